@@ -296,6 +296,94 @@ iskv_status iskv_select_prompt_blocks_noalloc(const void *keys, int32_t k_dtype,
                                               void *stream);
 
 /*
+ * Dense attention around the compressed cache. Algorithm 1 starts from a prompt whose exact
+ * attention has run, and Algorithm 3 step 9 attends over the cache that steps 7-8 reconstruct:
+ * iskv_prompt_attention() is the first, iskv_tree_attention() the second, for a tree of drafted
+ * tokens (one token is plain decoding), and iskv_rope() rotates the queries and keys of both.
+ *
+ * A block of row vectors: element (entry b, row i, head h, j) is data[b * batch + i * row + h * head
+ * + j], j < head_dim (strides in elements, not negative; the row stride of anything written is not
+ * 0). `batch` is ignored where there are no entries. float32, bf16 or fp16, all blocks of a call
+ * alike. Two-byte elements with head_dim a multiple of 8 up to 128, data 16-byte aligned and
+ * strides a multiple of 8 elements run on the tensor cores, everything else on CUDA cores.
+ */
+typedef struct {
+  void *data;
+  int64_t batch, row, head;
+} iskv_heads;
+
+/*
+ * Rotary embedding of n rows (Algorithm 3 step 8's rotation, as iskv_reconstruct applies it): in
+ * every head the pair (x[j], x[j + head_dim/2]) is rotated by the angle pos[i] *
+ * rope_theta^(-2j/head_dim), or by its negative when inverse != 0 (which takes rotated keys back to
+ * the rows the compression stores). Angles are reduced exactly in integers, products and sums are
+ * float32, rounded once.
+ * x, out  [n][n_heads][head_dim] dtype; out may be x (same data and strides), else they must not
+ *         overlap. pos [n] int32, any sign. head_dim even, 2..256; n_heads 1..1024.
+ */
+iskv_status iskv_rope(const iskv_heads *x, const int32_t *pos, int64_t n, int32_t n_heads,
+                      int32_t head_dim, double rope_theta, int32_t inverse, int32_t dtype,
+                      const iskv_heads *out, void *stream);
+
+/*
+ * Causal attention over whole prompts packed one behind another (the exact prompt attention that
+ * Algorithm 1 starts from). Sequence s is rows [cu_seqlens[s], cu_seqlens[s + 1]); for its token i
+ * and query head h (key/value head h / (n_q_heads / n_kv_heads)):
+ *   out_i = sum_{j <= i} softmax_j(scale q_i . k_j) v_j,   i, j in the sequence.
+ * q and k arrive rotated. Rows outside every sequence are neither read into a result nor written;
+ * a value or key that is not finite reaches only the rows that attend to it.
+ * q, out       [n_rows][n_q_heads][head_dim] dtype.  k, v [n_rows][n_kv_heads][head_dim].
+ * cu_seqlens   [n_seqs + 1] int32 device, not decreasing, inside [0, n_rows]; a sequence whose two
+ *              entries break that counts as empty and records ISKV_ERR_SHAPE in *status. NULL with
+ *              n_seqs == 1: one sequence of all rows.
+ * status       device int64, or NULL: bits (1 << code) are OR-ed in (ISKV_ERR_SHAPE,
+ *              ISKV_ERR_TIMEOUT).
+ * out must not overlap the inputs. 0 <= n_rows <= 2^24, 0 <= n_seqs <= 4096, n_q_heads a multiple
+ * of n_kv_heads, at most 64 query heads per key/value head, n_kv_heads <= 1024, head_dim 1..256,
+ * scale finite. Softmax and sums are float32; on the tensor cores the probabilities enter the
+ * second product in the element type.
+ */
+iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, const iskv_heads *v,
+                                  const int32_t *cu_seqlens, int32_t n_seqs, int64_t n_rows,
+                                  int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                  float scale, int32_t dtype, const iskv_heads *out,
+                                  int64_t *status, void *stream);
+
+/*
+ * Attention of a tree of drafted tokens over a dense cache (Algorithm 3 step 9 on the cache that
+ * iskv_reconstruct wrote). For each of `batch` entries, node i sees all n_cached[b] cached rows,
+ * itself and its ancestors in the tree:
+ *   out_i = sum over those j of softmax_j(scale q_i . k_j) v_j.
+ * q and the keys arrive rotated.
+ * q, out            [batch][n_nodes][n_q_heads][head_dim] dtype.
+ * k_draft, v_draft  [batch][n_nodes][n_kv_heads][head_dim]: the nodes' own keys and values.
+ * parents           [batch][n_nodes] int32 device: the index of an earlier node of the entry, or -1
+ *                   for a child of the last cached token. An entry below -1 is padding: padding and
+ *                   nodes whose chain reaches padding give zeros and are seen by no other node. An
+ *                   entry not below its own index counts as padding and records ISKV_ERR_SHAPE.
+ * k_cache, v_cache  [batch][n_cap][n_kv_heads][head_dim]; rows from n_cached[b] on are not read into
+ *                   a result.
+ * n_cached          [batch] int32 device, 0 <= n_cached[b] <= n_cap (a value outside is clamped and
+ *                   records ISKV_ERR_SHAPE), or NULL: all n_cap rows. It is read on the device, so a
+ *                   captured call follows the cache as it grows.
+ * status, scale, head counts, types as iskv_prompt_attention. 0 <= batch <= 4096, 0 <= n_nodes <=
+ * 128, 0 <= n_cap < 2^31. out must not overlap the inputs.
+ * ws                iskv_tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads, head_dim)
+ *                   bytes, 256-byte aligned (partial results of units cut between CTAs); calls that
+ *                   may overlap on the device need one each.
+ */
+size_t iskv_tree_attention_workspace_size(int32_t n_nodes, int32_t n_q_heads, int32_t n_kv_heads,
+                                          int32_t head_dim);
+iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
+                                const iskv_heads *v_draft, const int32_t *parents,
+                                const iskv_heads *k_cache, const iskv_heads *v_cache,
+                                const int32_t *n_cached, int32_t batch, int32_t n_nodes,
+                                int64_t n_cap, int32_t n_q_heads, int32_t n_kv_heads,
+                                int32_t head_dim, float scale, int32_t dtype,
+                                const iskv_heads *out, int64_t *status, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/*
  * Cache policy: the exact rows of one side (K or V) of one (sequence, layer), and when its pending
  * rows are folded (Section 3.1, Section 3.2; Algorithm 1 steps 5-9, Algorithm 3 steps 1-6).
  *
@@ -460,7 +548,8 @@ iskv_status iskv_get_status(const iskv_lowrank *h, int64_t *k, int64_t *n, int64
  * Instrumentation (no counterpart on the pages; measurement support). When stage timing is on,
  * every entry point records CUDA events on its own stream around each internal stage (fold:
  * projection, residual QR + SVD, core SVD, basis rotation, coordinate rotation, write-back;
- * reorth; reconstruction; selection; decode attention; cache step: append and eviction).
+ * reorth; reconstruction; selection; decode attention; cache step: append and eviction; rotary
+ * embedding; prompt and tree attention).
  * iskv_stage_read() waits for those events and returns the
  * accumulated milliseconds and call counts per stage (arrays of iskv_stage_count() entries, host
  * memory). iskv_stage_timing() returns the previous setting. iskv_launch_count() is the number of

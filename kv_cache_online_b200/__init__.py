@@ -16,7 +16,8 @@ import math
 import torch
 
 from . import _lib
-from ._lib import ISKV_BF16, ISKV_F16, ISKV_F32, IskvError, IskvExactTable, IskvLowRank  # noqa: F401
+from ._lib import (ISKV_BF16, ISKV_F16, ISKV_F32, IskvError, IskvExactTable,  # noqa: F401
+                   IskvHeads, IskvLowRank)
 
 _DT = {torch.float32: ISKV_F32, torch.bfloat16: ISKV_BF16, torch.float16: ISKV_F16}
 _TD = {ISKV_F32: torch.float32, ISKV_BF16: torch.bfloat16, ISKV_F16: torch.float16}
@@ -313,6 +314,163 @@ def decode_attention(k_hist, v_hist, k_exact, k_exact_pos, v_exact, v_exact_pos,
     return decode_attention_batched([k_hist], [v_hist], [k_exact], [k_exact_pos], [v_exact],
                                     [v_exact_pos], [n_total], [q], n_kv_heads, head_dim, theta,
                                     scale, None if out is None else [out], ws, stream)[0]
+
+
+# ------------------------------------------------------------------------------------------------
+# Dense attention around the compressed cache: the rotary embedding, the prompt's exact attention
+# (where Algorithm 1 starts) and drafted tokens over a reconstructed cache (Algorithm 3 step 9).
+
+class _On:
+    """The device and stream of a call: ``with _On(device, stream) as s`` makes the device current
+    and, for a given stream, allocates on it."""
+
+    def __init__(self, device, stream):
+        self.ctx = None
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError("the stream belongs to another device than the tensors")
+            self.ctx = torch.cuda.stream(stream)  # also makes its device current
+        elif device.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> IskvHeads:
+    """``t`` ([batch,] row, head, head_dim) as an ``iskv_heads``; its last axis is contiguous."""
+    if t.device != device or not t.is_cuda:
+        raise ValueError(f"{name}: all tensors must live on one CUDA device")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    st = t.stride()
+    if st[-1] != 1 and shape[-1] > 1:
+        raise ValueError(f"{name}: the last axis must be contiguous")
+    # The stride of an axis of length one is never used; torch leaves it arbitrary.
+    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], shape[:-1])]
+    if len(lead) == 2:
+        lead.insert(0, 0)
+    return IskvHeads(t.data_ptr(), *lead)
+
+
+def _ints(t: torch.Tensor, name: str, shape, device) -> int:
+    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous() \
+            or tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
+    return t.data_ptr()
+
+
+def _status_word(t, device):
+    if t is None:
+        return None
+    if t.device != device or t.dtype != torch.int64 or t.numel() < 1:
+        raise ValueError(f"status must be an int64 tensor on {device}")
+    return t.data_ptr()
+
+
+def _rank(t: torch.Tensor, name: str, n: int):
+    if t.dim() != n:
+        raise ValueError(f"{name}: {t.dim()} axes, expected {n}")
+    return tuple(t.shape)
+
+
+def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None, stream=None):
+    """Rotate-half rotary embedding of ``x`` (n, heads, head_dim) at positions ``pos`` (n,) int32,
+    as :func:`reconstruct` rotates keys; ``inverse`` turns rotated rows back (the rows that
+    :func:`cache_prefill` and the folds take). ``out`` may be ``x``."""
+    shape = _rank(x, "x", 3)
+    n, heads, hd = shape
+    dev = x.device
+    hx = _heads(x, "x", shape, x.dtype, dev)
+    dt = _dt(x)
+    pp = _ints(pos, "pos", (n,), dev)
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=x.dtype, device=dev)
+        ho = _heads(out, "out", shape, x.dtype, dev)
+        _lib.check(_lib.load().iskv_rope(hx, pp, n, heads, hd, theta, inverse, dt, ho, s), "rope")
+    return out
+
+
+def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None, stream=None):
+    """Causal attention over whole prompts packed one behind another: ``q`` (rows, n_q, head_dim),
+    ``k`` and ``v`` (rows, n_kv, head_dim), rotated; sequence ``s`` is rows ``cu_seqlens[s]`` to
+    ``cu_seqlens[s + 1]`` (int32 on the device; None: one sequence). Returns the outputs in ``q``'s
+    shape and dtype; rows outside every sequence are not written. ``status``: an int64 tensor that
+    collects error bits."""
+    shape = _rank(q, "q", 3)
+    rows, nq, hd = shape
+    nkv = _rank(k, "k", 3)[1]
+    dev, dtype = q.device, q.dtype
+    dt = _dt(q)
+    hq = _heads(q, "q", shape, dtype, dev)
+    hk = _heads(k, "k", (rows, nkv, hd), dtype, dev)
+    hv = _heads(v, "v", (rows, nkv, hd), dtype, dev)
+    sw = _status_word(status, dev)
+    with _On(dev, stream) as s:
+        seqs, cp = 1, None
+        if cu_seqlens is not None:
+            seqs = max(cu_seqlens.numel() - 1, 0)
+            cp = _ints(cu_seqlens, "cu_seqlens", (seqs + 1,), dev)
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        ho = _heads(out, "out", shape, dtype, dev)
+        _lib.check(_lib.load().iskv_prompt_attention(
+            hq, hk, hv, cp, seqs, rows, nq, nkv, hd,
+            1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, s), "prompt_attention")
+    return out
+
+
+def tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads, head_dim) -> int:
+    return int(_lib.load().iskv_tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads,
+                                                              head_dim))
+
+
+def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None, scale=None,
+                   out=None, status=None, ws=None, stream=None):
+    """Attention of trees of drafted tokens over dense caches (what :func:`reconstruct_batched`
+    writes): ``q`` (batch, nodes, n_q, head_dim); ``k_draft``, ``v_draft`` (batch, nodes, n_kv,
+    head_dim), the nodes' own rows; ``parents`` (batch, nodes) int32, an earlier node, -1 for a
+    child of the last cached token, below -1 for padding; ``k_cache``, ``v_cache`` (batch, n_cap,
+    n_kv, head_dim) with ``n_cached`` (batch,) int32 rows in use (None: all). Queries and keys are
+    rotated. Node ``i`` sees the cached rows, itself and its ancestors; padding gives zeros. One node
+    with parent -1 is plain decoding. Returns the outputs in ``q``'s shape and dtype."""
+    shape = _rank(q, "q", 4)
+    b, t, nq, hd = shape
+    _, cap, nkv, _ = _rank(k_cache, "k_cache", 4)
+    dev, dtype = q.device, q.dtype
+    dt = _dt(q)
+    hq = _heads(q, "q", shape, dtype, dev)
+    hkd = _heads(k_draft, "k_draft", (b, t, nkv, hd), dtype, dev)
+    hvd = _heads(v_draft, "v_draft", (b, t, nkv, hd), dtype, dev)
+    hkc = _heads(k_cache, "k_cache", (b, cap, nkv, hd), dtype, dev)
+    hvc = _heads(v_cache, "v_cache", (b, cap, nkv, hd), dtype, dev)
+    pp = _ints(parents, "parents", (b, t), dev)
+    npp = None if n_cached is None else _ints(n_cached, "n_cached", (b,), dev)
+    sw = _status_word(status, dev)
+    lib = _lib.load()
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=dev)
+        ho = _heads(out, "out", shape, dtype, dev)
+        if ws is None:
+            # A buffer of this call's own, from the stream's pool: calls on several streams and
+            # captured graphs never share one.
+            ws = torch.empty(lib.iskv_tree_attention_workspace_size(t, nq, nkv, hd),
+                             dtype=torch.uint8, device=dev)
+        _lib.check(lib.iskv_tree_attention(
+            hq, hkd, hvd, pp, hkc, hvc, npp, b, t, cap, nq, nkv, hd,
+            1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, ws.data_ptr(),
+            ws.numel() * ws.element_size(), s), "tree_attention")
+    return out
 
 
 def select_workspace_size(L, n_heads, block=8) -> int:

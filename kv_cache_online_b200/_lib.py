@@ -35,6 +35,14 @@ class IskvExactTable(ctypes.Structure):
                 ("hist_rows", c_i64), ("refit_done", c_i64)]
 
 
+class IskvHeads(ctypes.Structure):
+    """Mirror of ``iskv_heads``."""
+
+    _fields_ = [("data", c_vp), ("batch", c_i64), ("row", c_i64), ("head", c_i64)]
+
+
+c_hp = ctypes.POINTER(IskvHeads)
+
 # name -> (restype, argtypes)
 SIGNATURES = {
     "iskv_abi_version": (c_i32, []),
@@ -80,6 +88,13 @@ SIGNATURES = {
                                           c_i32, c_vp, c_vp, c_vp, c_vp, c_vp, c_sz, c_vp]),
     "iskv_select_prompt_blocks_noalloc": (c_i32, [c_vp, c_i32, c_i64, c_i32, c_i32, c_i32, c_i32,
                                                   c_i32, c_i32, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "iskv_rope": (c_i32, [c_hp, c_vp, c_i64, c_i32, c_i32, c_f64, c_i32, c_i32, c_hp, c_vp]),
+    "iskv_prompt_attention": (c_i32, [c_hp, c_hp, c_hp, c_vp, c_i32, c_i64, c_i32, c_i32, c_i32,
+                                      c_f32, c_i32, c_hp, c_vp, c_vp]),
+    "iskv_tree_attention_workspace_size": (c_sz, [c_i32, c_i32, c_i32, c_i32]),
+    "iskv_tree_attention": (c_i32, [c_hp, c_hp, c_hp, c_vp, c_hp, c_hp, c_vp, c_i32, c_i32, c_i64,
+                                    c_i32, c_i32, c_i32, c_f32, c_i32, c_hp, c_vp, c_vp, c_sz,
+                                    c_vp]),
     "iskv_cache_prefill_workspace_size": (c_sz, [c_i32]),
     "iskv_cache_prefill": (c_i32, [ctypes.POINTER(IskvExactTable), c_vp, c_i32, c_i64, c_vp, c_i64,
                                    c_i32, c_vp, c_vp, ctypes.POINTER(c_i64), c_vp, c_sz, c_vp]),

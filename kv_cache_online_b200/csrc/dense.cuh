@@ -1,0 +1,210 @@
+// Work decomposition shared by the dense-attention kernels.
+//
+// Grouped heads: the `group` query heads that read one key/value head are packed into rows, row
+// r = (token, query head of the group) = (r / group, r % group), so that a tile's rows share every
+// key and value and a single token still fills `group` rows.
+//
+// Prompt: a unit is (sequence, key/value head, block of ROWS packed rows) and runs over the keys
+// up to its last token. CTAs take units in descending row-block index over all sequences (the
+// longest runs first: the block scheduler then packs the short ones behind them).
+//
+// Tree: a unit is (batch entry, key/value head, row block); its keys are the cached rows, in tiles
+// of KT, followed by the drafted nodes in tiles of KT. All units' tiles form one line that is cut
+// into gridDim.x equal shares, whatever the lengths; units cut in two or more are joined by
+// k_dense_join.
+#pragma once
+
+#include "common.cuh"
+#include "dense.h"
+
+namespace iskv {
+namespace dense {
+
+// status: one int64 word (or NULL), bit (1 << code).
+ISKV_DEV void report(int64_t *status, int code) {
+  if (status) atomicOr(reinterpret_cast<unsigned long long *>(status), 1ull << code);
+}
+
+// One unit's place: tiles [t0, t1) of its n_tiles.
+struct Unit {
+  int b;          // sequence / batch entry; -1: nothing to do
+  int kvh;
+  int row0;       // first packed row of the block
+  int n_rows;     // packed rows of the block (<= ROWS)
+  int64_t base;   // prompt: first packed row of the sequence in q / k / v
+  int len;        // prompt: tokens of the sequence; tree: cached rows
+  int cache_tiles;  // tree: key tiles over the cache (the drafted nodes' follow)
+  int n_tiles;
+  int t0, t1;
+};
+
+// Rows [lo, hi) of sequence s; an inconsistent entry counts as empty and is reported.
+ISKV_DEV int seq_len(const DenseArgs &a, int s, int64_t &lo) {
+  if (!a.cu) {  // one sequence of all rows
+    lo = 0;
+    return (int)a.rows;
+  }
+  const int64_t b = a.cu[s], e = a.cu[s + 1];
+  lo = b;
+  if (b < 0 || e < b || e > a.rows) {
+    report(a.status, ISKV_ERR_SHAPE);
+    return 0;
+  }
+  return (int)(e - b);
+}
+
+// Whole warp: the rank-th unit (without its head) of a prompt call. F(m) = sum over sequences of
+// max(blocks - m, 0) counts the blocks with index >= m; the unit has the largest m with
+// F(m) > rank.
+template <int ROWS>
+ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
+  const int lane = threadIdx.x & 31;
+  auto blocks = [&](int s) {
+    int64_t lo;
+    return s < a.batch ? (int)(((int64_t)seq_len(a, s, lo) * a.group + ROWS - 1) / ROWS) : 0;
+  };
+  const int mine = blocks(lane);  // the first 32 sequences stay in registers
+  int top = mine;
+  for (int s = 32 + lane; s < a.batch; s += 32) top = max(top, blocks(s));
+  top = __reduce_max_sync(0xffffffffu, top);
+  auto F = [&](int m) {
+    int n = max(mine - m, 0);
+    for (int s = 32 + lane; s < a.batch; s += 32) n += max(blocks(s) - m, 0);
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  if (top == 0 || F(0) <= rank) return false;
+  int lo = 0, hi = top, above = 0;  // F(lo) > rank >= F(hi) = above
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2, f = F(mid);
+    if (f > rank) {
+      lo = mid;
+    } else {
+      hi = mid;
+      above = f;
+    }
+  }
+  int skip = rank - above;  // among the sequences with more than lo blocks
+  for (int s0 = 0; s0 < a.batch; s0 += 32) {
+    const unsigned has = __ballot_sync(0xffffffffu, (s0 == 0 ? mine : blocks(s0 + lane)) > lo);
+    const int n = __popc(has);
+    if (skip >= n) {
+      skip -= n;
+      continue;
+    }
+    u.b = s0 + (int)__fns(has, 0, skip + 1);
+    break;
+  }
+  u.len = seq_len(a, u.b, u.base);
+  u.row0 = lo * ROWS;
+  u.n_rows = min(ROWS, u.len * a.group - u.row0);
+  return true;
+}
+
+// Tokens of the first and last row of a block.
+ISKV_DEV int first_token(const DenseArgs &a, const Unit &u) { return u.row0 / a.group; }
+ISKV_DEV int last_token(const DenseArgs &a, const Unit &u) {
+  return (u.row0 + u.n_rows - 1) / a.group;
+}
+
+ISKV_DEV int cached_rows(const DenseArgs &a, int b) {
+  if (!a.n_cached) return (int)a.rows;
+  const int n = a.n_cached[b];
+  if (n < 0 || n > a.rows) {
+    report(a.status, ISKV_ERR_SHAPE);
+    return n < 0 ? 0 : (int)a.rows;
+  }
+  return n;
+}
+
+template <int KT>
+ISKV_DEV int64_t entry_tiles(const DenseArgs &a, int b, int blocks) {
+  return ((int64_t)(cached_rows(a, b) + KT - 1) / KT + (a.nodes + KT - 1) / KT) * a.n_kv * blocks;
+}
+
+// Whole warp: tiles of all entries.
+template <int KT>
+ISKV_DEV int64_t total_tiles(const DenseArgs &a, int blocks) {
+  int64_t n = 0;
+  for (int b = threadIdx.x & 31; b < a.batch; b += 32) n += entry_tiles<KT>(a, b, blocks);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// Whole warp: the entry that holds tile x of the line, and the line position of its first tile.
+template <int KT>
+ISKV_DEV int find_entry(const DenseArgs &a, int blocks, int64_t x, int64_t &start) {
+  const int lane = threadIdx.x & 31;
+  int64_t before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+    const int64_t n = b0 + lane < a.batch ? entry_tiles<KT>(a, b0 + lane, blocks) : 0;
+    int64_t sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += t;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      start = before + __shfl_sync(0xffffffffu, sum - n, l);
+      return b0 + l;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  start = before;
+  return -1;
+}
+
+// The share of CTA c: line positions [share(c), share(c + 1)); and the CTA that holds position x.
+ISKV_DEV int64_t share_begin(int64_t total, int grid, int c) { return total * c / grid; }
+ISKV_DEV int share_owner(int64_t total, int grid, int64_t x) {
+  return (int)(((x + 1) * grid - 1) / total);
+}
+
+// The unit holding line position x of entry b (first tile at line position start), cut to the
+// share's end.
+template <int ROWS, int KT>
+ISKV_DEV void tree_unit(const DenseArgs &a, int b, int64_t start, int64_t x, int64_t end, Unit &u) {
+  u.b = b;
+  u.base = 0;
+  u.len = cached_rows(a, b);
+  u.cache_tiles = (u.len + KT - 1) / KT;
+  u.n_tiles = u.cache_tiles + (a.nodes + KT - 1) / KT;
+  const int all_rows = a.nodes * a.group, blocks = (all_rows + ROWS - 1) / ROWS;
+  const int64_t off = x - start;
+  const int idx = (int)(off / u.n_tiles);
+  u.kvh = idx / blocks;
+  u.row0 = (idx % blocks) * ROWS;
+  u.n_rows = min(ROWS, all_rows - u.row0);
+  u.t0 = (int)(off - (int64_t)idx * u.n_tiles);
+  const int64_t left = end - x;
+  u.t1 = (int)min((int64_t)u.n_tiles, u.t0 + left);
+}
+
+// Bits of the nodes that node i of entry b sees: itself and its ancestors. parents[i] is the
+// index of an earlier node, or -1 (a child of the last cached token); an entry below -1 is padding.
+// Padding, a node whose chain reaches padding, and an entry that is not below its own index
+// (reported) see nothing.
+ISKV_DEV void node_mask(const DenseArgs &a, int b, int i, uint32_t (&m)[4]) {
+  const int32_t *par = a.parents + (int64_t)b * a.nodes;
+  m[0] = m[1] = m[2] = m[3] = 0;
+  int cur = i;
+  bool live = true;
+  while (cur >= 0) {
+    const int up = par[cur];
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+      if ((cur >> 5) == w) m[w] |= 1u << (cur & 31);
+    if (up >= cur) report(a.status, ISKV_ERR_SHAPE);
+    if (up >= cur || up < -1) {
+      live = false;
+      break;
+    }
+    cur = up;
+  }
+  if (!live) m[0] = m[1] = m[2] = m[3] = 0;
+}
+
+}  // namespace dense
+}  // namespace iskv

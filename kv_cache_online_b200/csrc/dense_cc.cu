@@ -1,0 +1,430 @@
+// Dense attention on the CUDA cores: float32, and two-byte elements whose shape or alignment the
+// tensor-core kernel does not take. Also the join of a tree call's partial results.
+//
+// One pass over the keys with a running maximum m and sum l per row (x = scale log2(e) q.k):
+//   m' = max(m, max_j x_j);  p_j = 2^(x_j - m');  l' = l 2^(m - m') + sum p_j;
+//   O' = O 2^(m - m') + sum_j p_j v_j;  out = O / l.
+//
+// FP32-FMA bound: 4 hd flops per visible pair on 128 lanes per SM. A block of 256 threads owns 64
+// rows and walks tiles of 64 keys; thread (ty, tx) holds scores of rows 4 ty + i and keys
+// tx + 16 j, and output columns 4 tx + 64 c, so that a score step reads 8 float4 for 64 FMAs and a
+// value step 4 + HD/16 float4 for HD FMAs, without bank conflicts (row strides of HD + 4 floats).
+// All operands are float32 in shared memory, products and statistics float32.
+#include "dense.cuh"
+#include "profiling.h"
+
+namespace iskv {
+namespace {
+
+using namespace dense;
+
+constexpr int ROWS = DENSE_CC_ROWS, KT = 64, NT = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+
+template <int HD>
+struct Smem {
+  static constexpr int LD = HD + 4;
+  float q[ROWS][LD], k[KT][LD], v[KT][LD];
+  float p[ROWS][KT + 4];
+  uint32_t mask[DENSE_MAX_NODES][4];
+  Unit unit;
+  int64_t pos, end, total;
+};
+
+ISKV_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Element offset of (entry, row, head).
+ISKV_DEV int64_t at(const iskv_heads &x, int64_t b, int64_t row, int64_t head) {
+  return b * x.batch + row * x.row + head * x.head;
+}
+
+// `n` rows of one head as float32 rows of shared memory; rows from n on and columns from hd on are
+// zero. VEC: 16-byte loads (hd and strides are multiples of a vector, the base is aligned).
+template <typename T, int HD, bool VEC>
+ISKV_DEV void load_rows(float (*dst)[HD + 4], const T *src, int64_t stride, int n, int hd) {
+  if constexpr (VEC) {
+    constexpr int V = 16 / sizeof(T), C = HD / V;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < KT * C; i += NT) {
+      const int r = i / C, c = i % C * V;
+      alignas(16) T x[V];
+      if (r < n && c < hd)
+        *reinterpret_cast<uint4 *>(x) = *reinterpret_cast<const uint4 *>(src + r * stride + c);
+      else
+        *reinterpret_cast<uint4 *>(x) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < V; e += 4)
+        *reinterpret_cast<float4 *>(&dst[r][c + e]) =
+            make_float4(to_f(x[e]), to_f(x[e + 1]), to_f(x[e + 2]), to_f(x[e + 3]));
+    }
+  } else {
+    for (int i = threadIdx.x; i < KT * HD; i += NT) {
+      const int r = i / HD, c = i % HD;
+      dst[r][c] = r < n && c < hd ? to_f(src[r * stride + c]) : 0.f;
+    }
+  }
+}
+
+template <typename T, int HD, bool TREE, bool VEC>
+ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
+  constexpr int NC = HD / 64;
+  const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  const int hd = a.head_dim;
+  // Non-negative factor on the scores; the scale's sign goes into the queries.
+  const float c = fabsf(a.scale) * LOG2E;
+  const int64_t row_base = TREE ? 0 : u.base;
+
+  for (int i = threadIdx.x; i < ROWS * HD; i += NT) {
+    const int r = i / HD, col = i % HD;
+    float x = 0.f;
+    if (r < u.n_rows && col < hd) {
+      const int pr = u.row0 + r;
+      x = to_f(static_cast<const T *>(a.q.data)[at(a.q, TREE ? u.b : 0, row_base + pr / a.group,
+                                                   (int64_t)u.kvh * a.group + pr % a.group) + col]);
+    }
+    sm.q[r][col] = a.scale < 0.f ? -x : x;
+  }
+  if constexpr (TREE) {
+    if (threadIdx.x < a.nodes) {
+      uint32_t m[4];
+      node_mask(a, u.b, threadIdx.x, m);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sm.mask[threadIdx.x][w] = m[w];
+    }
+  }
+  int tok[4];  // prompt: the row's token; tree: its node
+  float m[4], l[4], o[4][NC][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    tok[i] = (u.row0 + min(ty * 4 + i, u.n_rows - 1)) / a.group;
+    m[i] = -INFINITY;
+    l[i] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NC; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
+  }
+
+  for (int t = u.t0; t < u.t1; ++t) {
+    const bool draft = TREE && t >= u.cache_tiles;
+    const int k0 = (draft ? t - u.cache_tiles : t) * KT;  // first key of the tile
+    const int n_keys = min(KT, (draft ? a.nodes : u.len) - k0);
+    const iskv_heads &K = TREE && !draft ? a.kc : a.k, &V = TREE && !draft ? a.vc : a.v;
+    __syncthreads();  // the previous tile's keys, values and probabilities are no longer read
+    load_rows<T, HD, VEC>(sm.k, static_cast<const T *>(K.data) +
+                          at(K, TREE ? u.b : 0, row_base + k0, u.kvh), K.row, n_keys, hd);
+    load_rows<T, HD, VEC>(sm.v, static_cast<const T *>(V.data) +
+                          at(V, TREE ? u.b : 0, row_base + k0, u.kvh), V.row, n_keys, hd);
+    __syncthreads();
+
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < HD; d += 4) {
+      float4 qv[4], kv[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty * 4 + i][d]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][d]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+          s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+          s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+          s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+        }
+    }
+    // Pairs the mask leaves out have p = -1 in shared memory: the value step skips them, so that
+    // a value that is not finite cannot reach a row that does not see it.
+    const bool masked = n_keys < KT || draft || (!TREE && k0 + KT > first_token(a, u) + 1);
+    uint32_t seen = 0xffffu;
+    if (masked) {
+      seen = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = k0 + tx + 16 * j;
+          bool see = tx + 16 * j < n_keys;
+          if (draft) see = see && (sm.mask[tok[i]][(key >> 5) & 3] >> (key & 31) & 1);
+          if (!TREE) see = see && key <= tok[i];
+          if (see) seen |= 1u << (i * 4 + j);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float top = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = seen >> (i * 4 + j) & 1 ? s[i][j] * c : -INFINITY;
+        top = fmaxf(top, s[i][j]);
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+      const float mn = fmaxf(m[i], top);
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      const float alpha = ex2(m[i] - ref);  // 0 while nothing was seen
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = ex2(s[i][j] - ref);
+        const bool see = seen >> (i * 4 + j) & 1;
+        if (see) sum += p;
+        sm.p[ty * 4 + i][tx + 16 * j] = see ? p : -1.f;
+      }
+#pragma unroll
+      for (int w = 8; w > 0; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+      l[i] = l[i] * alpha + sum;
+      m[i] = mn;
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[i][n][e] *= alpha;
+    }
+    __syncwarp();  // a row's probabilities are written and read by the same half-warp
+    auto values = [&](auto guarded) {
+#pragma unroll 2
+      for (int k = 0; k < KT; k += 4) {
+        float4 p[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) p[i] = *reinterpret_cast<const float4 *>(&sm.p[ty * 4 + i][k]);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+          for (int n = 0; n < NC; ++n) {
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.v[k + kk][tx * 4 + 64 * n]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+              if (decltype(guarded)::value && w < 0.f) continue;
+              o[i][n][0] = fmaf(w, v.x, o[i][n][0]);
+              o[i][n][1] = fmaf(w, v.y, o[i][n][1]);
+              o[i][n][2] = fmaf(w, v.z, o[i][n][2]);
+              o[i][n][3] = fmaf(w, v.w, o[i][n][3]);
+            }
+          }
+        }
+      }
+    };
+    if (masked) values(std::true_type{});
+    else values(std::false_type{});
+  }
+
+  const bool whole = !TREE || (u.t0 == 0 && u.t1 == u.n_tiles);
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= u.n_rows) continue;
+      bool live = true;  // padding nodes give zeros
+      if constexpr (TREE)
+        live = (sm.mask[tok[i]][0] | sm.mask[tok[i]][1] | sm.mask[tok[i]][2] | sm.mask[tok[i]][3]);
+      const int pr = u.row0 + r;
+      T *out = static_cast<T *>(a.out.data) + at(a.out, TREE ? u.b : 0, row_base + pr / a.group,
+                                                 (int64_t)u.kvh * a.group + pr % a.group);
+      const float inv = 1.f / l[i];
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int col = tx * 4 + 64 * n + e;
+          if (col < hd) out[col] = from_f<T>(live && l[i] != 0.f ? o[i][n][e] * inv : 0.f);
+        }
+    }
+  } else {
+    const int slot = 2 * blockIdx.x + (u.t0 > 0 ? 0 : 1);
+    float *ws = static_cast<float *>(a.ws) + slot * dense_slot_floats(ROWS, HD);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty * 4 + i;
+      if (r >= u.n_rows) continue;
+#pragma unroll
+      for (int n = 0; n < NC; ++n)
+        reinterpret_cast<float4 *>(ws)[(tx + 16 * n) * ROWS + r] =
+            make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
+      if (tx == 0) {
+        ws[ROWS * HD + r] = m[i];
+        ws[ROWS * (HD + 1) + r] = l[i];
+      }
+    }
+  }
+}
+
+template <typename T, int HD, bool TREE, bool VEC>
+__global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseArgs a) {
+  extern __shared__ __align__(16) char raw[];
+  Smem<HD> &sm = *reinterpret_cast<Smem<HD> *>(raw);
+  if constexpr (!TREE) {
+    if (threadIdx.x < 32) {
+      Unit u;
+      u.b = -1;
+      if (find_prompt_unit<ROWS>(a, blockIdx.x / a.n_kv, u)) {
+        u.kvh = blockIdx.x % a.n_kv;
+        u.t0 = 0;
+        u.t1 = u.n_tiles = last_token(a, u) / KT + 1;
+      }
+      if (threadIdx.x == 0) sm.unit = u;
+    }
+    __syncthreads();
+    const Unit u = sm.unit;
+    if (u.b >= 0) run_unit<T, HD, false, VEC>(a, sm, u);
+  } else {
+    const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
+    int64_t x = 0, end = 0, start = 0;
+    for (bool first = true;; first = false) {
+      __syncthreads();  // the previous unit's place is no longer read
+      if (threadIdx.x < 32) {
+        if (first) {
+          const int64_t total = total_tiles<KT>(a, blocks);
+          x = share_begin(total, gridDim.x, blockIdx.x);
+          end = share_begin(total, gridDim.x, blockIdx.x + 1);
+        }
+        Unit u;
+        u.b = -1;
+        if (x < end) {
+          const int b = find_entry<KT>(a, blocks, x, start);
+          tree_unit<ROWS, KT>(a, b, start, x, end, u);
+          x += u.t1 - u.t0;
+        }
+        if (threadIdx.x == 0) sm.unit = u;
+      }
+      __syncthreads();
+      const Unit u = sm.unit;
+      if (u.b < 0) break;
+      run_unit<T, HD, true, VEC>(a, sm, u);
+    }
+  }
+}
+
+// One warp: 32 rows of one four-column group of one unit; sums the unit's parts with weights
+// 2^(m_i - max m).
+template <typename T>
+__global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
+                                                    int ROWS_, int KT_, int hd_pad) {
+  const int rows_all = a.nodes * a.group, blocks = (rows_all + ROWS_ - 1) / ROWS_;
+  const int lane = threadIdx.x & 31;
+  const int unit = blockIdx.x, kvh = unit / blocks % a.n_kv, blk = unit % blocks;
+  const int b = unit / blocks / a.n_kv;
+  auto tiles = [&](int e) {
+    return (int64_t)(cached_rows(a, e) + KT_ - 1) / KT_ + (a.nodes + KT_ - 1) / KT_;
+  };
+  int64_t before = 0, total = 0;
+  for (int e = lane; e < a.batch; e += 32) {
+    const int64_t n = tiles(e) * a.n_kv * blocks;
+    total += n;
+    if (e < b) before += n;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(0xffffffffu, total, o);
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+  }
+  const int64_t n = tiles(b), u0 = before + ((int64_t)kvh * blocks + blk) * n, u1 = u0 + n;
+  const int c0 = share_owner(total, grid, u0), c1 = share_owner(total, grid, u1 - 1);
+  if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
+  const int n_rows = min(ROWS_, rows_all - blk * ROWS_);
+  const int chunks = (n_rows + 31) / 32, cols = (a.head_dim + 3) / 4;
+  const size_t slot_floats = dense_slot_floats(ROWS_, hd_pad);
+  const float *ws = static_cast<const float *>(a.ws);
+  const int warp = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
+  if (warp >= chunks * cols) return;
+  const int r = warp / cols * 32 + lane, c4 = warp % cols;
+  if (r >= n_rows) return;
+  const int pr = blk * ROWS_ + r, node = pr / a.group;
+  float m = -INFINITY;
+  auto slot = [&](int c) {
+    return ws + (2 * c + (share_begin(total, grid, c) > u0 ? 0 : 1)) * slot_floats;
+  };
+  for (int c = c0; c <= c1; ++c)
+    if (share_begin(total, grid, c + 1) > share_begin(total, grid, c))
+      m = fmaxf(m, slot(c)[(size_t)ROWS_ * hd_pad + r]);
+  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c = c0; c <= c1; ++c) {
+    if (share_begin(total, grid, c + 1) <= share_begin(total, grid, c)) continue;
+    const float *w = slot(c);
+    const float mi = w[(size_t)ROWS_ * hd_pad + r], li = w[(size_t)ROWS_ * (hd_pad + 1) + r];
+    if (mi == -INFINITY && !(li != li)) continue;  // a part that saw nothing
+    const float f = exp2f(mi - m);
+    const float4 v = reinterpret_cast<const float4 *>(w)[(size_t)c4 * ROWS_ + r];
+    l = fmaf(li, f, l);
+    o[0] = fmaf(v.x, f, o[0]);
+    o[1] = fmaf(v.y, f, o[1]);
+    o[2] = fmaf(v.z, f, o[2]);
+    o[3] = fmaf(v.w, f, o[3]);
+  }
+  uint32_t mask[4];
+  node_mask(a, b, node, mask);
+  const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) && l != 0.f;
+  T *out = static_cast<T *>(a.out.data) +
+           at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (c4 * 4 + e < a.head_dim) out[c4 * 4 + e] = from_f<T>(live ? o[e] / l : 0.f);
+}
+
+template <typename T, int HD, bool TREE, bool VEC>
+cudaError_t run(const DenseArgs &a, int grid, cudaStream_t s) {
+  auto *kernel = k_dense_cc<T, HD, TREE, VEC>;
+  const int smem = (int)sizeof(Smem<HD>);
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, NT, smem, s>>>(a);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, cudaStream_t s) {
+  const int blocks = (a.nodes * a.group + rows - 1) / rows;
+  const int warps = ((rows < a.nodes * a.group ? rows : a.nodes * a.group) + 31) / 32 *
+                    ((a.head_dim + 3) / 4);
+  const dim3 g((unsigned)(a.batch * a.n_kv * blocks), (unsigned)((warps + 3) / 4));
+  with_dtype(a.dtype, [&](auto tag) {
+    k_dense_join<decltype(tag)><<<g, 128, 0, s>>>(a, grid, rows, keys, dense_hd_pad(a.head_dim));
+  });
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense_cc(const DenseArgs &a, cudaStream_t s) {
+  const int64_t v = a.dtype == ISKV_F32 ? 4 : 8;
+  auto wide = [&](const iskv_heads &x) {
+    return a.head_dim % v == 0 && reinterpret_cast<uintptr_t>(x.data) % 16 == 0 &&
+           (!a.tree || x.batch % v == 0) && x.row % v == 0 && x.head % v == 0;
+  };
+  const bool vec = wide(a.k) && wide(a.v) && (!a.tree || (wide(a.kc) && wide(a.vc)));
+  const int64_t grid = a.tree ? DENSE_CC_GRID
+                              : (a.rows * a.group / ROWS + a.batch) * (int64_t)a.n_kv;
+  if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+  cudaError_t e = cudaSuccess;
+  with_dtype(a.dtype, [&](auto tag) {
+    using T = decltype(tag);
+    auto width = [&](auto hd) {
+      constexpr int HD = decltype(hd)::value;
+      auto mode = [&](auto tree) {
+        constexpr bool TREE = decltype(tree)::value;
+        e = vec ? run<T, HD, TREE, true>(a, (int)grid, s) : run<T, HD, TREE, false>(a, (int)grid, s);
+      };
+      if (a.tree) mode(std::true_type{});
+      else mode(std::false_type{});
+    };
+    const int pad = dense_hd_pad(a.head_dim);
+    if (pad == 64) width(std::integral_constant<int, 64>{});
+    else if (pad == 128) width(std::integral_constant<int, 128>{});
+    else width(std::integral_constant<int, 256>{});
+  });
+  if (e == cudaSuccess && a.tree) e = launch_dense_join(a, (int)grid, ROWS, KT, s);
+  return e;
+}
+
+}  // namespace iskv

@@ -31,7 +31,7 @@ const char *kNames[ST_COUNT] = {
     "reconstruct.compressed",
     "reconstruct.exact", "select",            "job_upload",        "attention.prepare",
     "attention.scores", "attention.softmax",  "attention.values", "cache.append",
-    "cache.evict"};
+    "cache.evict",    "rope",                "prompt_attention",   "tree_attention"};
 
 cudaEvent_t take_event() {
   if (!g_free.empty()) {

@@ -32,6 +32,9 @@ enum Stage {
   ST_ATTN_VALUES,
   ST_CACHE_APPEND,
   ST_CACHE_EVICT,
+  ST_ROPE,
+  ST_PROMPT_ATTN,
+  ST_TREE_ATTN,
   ST_COUNT
 };
 
