@@ -182,25 +182,34 @@ ISKV_DEV void tree_unit(const DenseArgs &a, int b, int64_t start, int64_t x, int
   u.t1 = (int)min((int64_t)u.n_tiles, u.t0 + left);
 }
 
-// Bits of the nodes that node i of entry b sees: itself and its ancestors. parents[i] is the
-// index of an earlier node, or -1 (a child of the last cached token); an entry below -1 is padding.
-// Padding, a node whose chain reaches padding, and an entry that is not below its own index
-// (reported) see nothing.
-ISKV_DEV void node_mask(const DenseArgs &a, int b, int i, uint32_t (&m)[4]) {
-  const int32_t *par = a.parents + (int64_t)b * a.nodes;
-  m[0] = m[1] = m[2] = m[3] = 0;
+// Whole warp: bits of the nodes that each lane's node i sees, given its entry's parents: itself and
+// its ancestors. par[i] is the index of an earlier node, or -1 (a child of the last cached token); an
+// entry below -1 is padding. Padding, a node whose chain reaches padding, and an entry that is not
+// below its own index (reported) see nothing. The parents sit in four registers of the warp, a step
+// up the chain is a shuffle.
+ISKV_DEV void node_mask(const DenseArgs &a, const int32_t *par, int i, uint32_t (&m)[4]) {
+  const int lane = threadIdx.x & 31;
+  int p[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    p[w] = w * 32 + lane < a.nodes ? par[w * 32 + lane] : -2;
+    m[w] = 0;
+  }
   int cur = i;
   bool live = true;
-  while (cur >= 0) {
-    const int up = par[cur];
+  while (__any_sync(0xffffffffu, live && cur >= 0)) {
+    int up = -1;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int x = __shfl_sync(0xffffffffu, p[w], cur & 31);
+      if ((cur >> 5) == w) up = x;
+    }
+    if (!live || cur < 0) continue;
 #pragma unroll
     for (int w = 0; w < 4; ++w)
       if ((cur >> 5) == w) m[w] |= 1u << (cur & 31);
     if (up >= cur) report(a.status, ISKV_ERR_SHAPE);
-    if (up >= cur || up < -1) {
-      live = false;
-      break;
-    }
+    if (up >= cur || up < -1) live = false;
     cur = up;
   }
   if (!live) m[0] = m[1] = m[2] = m[3] = 0;

@@ -49,6 +49,10 @@ inline int dense_hd_pad(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; 
 // CUDA-core kernel: float32 and whatever the tensor-core kernel does not take.
 constexpr int DENSE_CC_ROWS = 64;
 cudaError_t launch_dense_cc(const DenseArgs &a, cudaStream_t s);
+// Tensor-core kernel: two-byte elements, head_dim a multiple of 8 up to 128, 16-byte aligned rows.
+bool dense_tc_takes(const DenseArgs &a);
+// false: a tensor map could not be encoded and nothing was launched.
+bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e);
 // Joins the partial results of a tree call whose kernel ran `grid` CTAs over units of `rows` rows
 // and tiles of `keys` keys.
 cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, cudaStream_t s);

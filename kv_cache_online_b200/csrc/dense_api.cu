@@ -49,6 +49,12 @@ iskv_status check_status_word(const int64_t *status, const char *who) {
   return ISKV_OK;
 }
 
+cudaError_t launch_dense(const DenseArgs &a, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (dense_tc_takes(a) && launch_dense_tc(a, s, e)) return e;
+  return launch_dense_cc(a, s);
+}
+
 }  // namespace
 
 extern "C" {
@@ -141,7 +147,7 @@ iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, cons
   a.status = status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   stage_begin(s);
-  cudaError_t e = launch_dense_cc(a, s);
+  cudaError_t e = launch_dense(a, s);
   if (e != cudaSuccess) return cuda_fail(e, who);
   stage_mark(s, ST_PROMPT_ATTN);
   return ISKV_OK;
@@ -153,7 +159,10 @@ size_t iskv_tree_attention_workspace_size(int32_t n_nodes, int32_t n_q_heads, in
       n_q_heads % n_kv_heads || n_q_heads / n_kv_heads > 64 || head_dim < 1 || head_dim > 256)
     return 0;
   const size_t cc = 2 * DENSE_CC_GRID * dense_slot_floats(DENSE_CC_ROWS, dense_hd_pad(head_dim));
-  return cc * sizeof(float);
+  const int tc_rows = n_nodes * (n_q_heads / n_kv_heads) <= 128 ? 128 : 256;
+  const size_t tc =
+      head_dim <= 128 ? 2 * DENSE_TC_GRID * dense_slot_floats(tc_rows, dense_hd_pad(head_dim)) : 0;
+  return (cc > tc ? cc : tc) * sizeof(float);
 }
 
 iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
@@ -219,7 +228,7 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   a.ws = ws;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   stage_begin(s);
-  cudaError_t e = launch_dense_cc(a, s);
+  cudaError_t e = launch_dense(a, s);
   if (e != cudaSuccess) return cuda_fail(e, who);
   stage_mark(s, ST_TREE_ATTN);
   return ISKV_OK;

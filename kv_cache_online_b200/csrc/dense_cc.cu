@@ -89,9 +89,9 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
     sm.q[r][col] = a.scale < 0.f ? -x : x;
   }
   if constexpr (TREE) {
-    if (threadIdx.x < a.nodes) {
+    if (threadIdx.x < DENSE_MAX_NODES) {
       uint32_t m[4];
-      node_mask(a, u.b, threadIdx.x, m);
+      node_mask(a, a.parents + (int64_t)u.b * a.nodes, min((int)threadIdx.x, a.nodes - 1), m);
 #pragma unroll
       for (int w = 0; w < 4; ++w) sm.mask[threadIdx.x][w] = m[w];
     }
@@ -338,8 +338,10 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int warp = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
   if (warp >= chunks * cols) return;
   const int r = warp / cols * 32 + lane, c4 = warp % cols;
+  const int pr = blk * ROWS_ + min(r, n_rows - 1), node = pr / a.group;
+  uint32_t mask[4];
+  node_mask(a, a.parents + (int64_t)b * a.nodes, node, mask);
   if (r >= n_rows) return;
-  const int pr = blk * ROWS_ + r, node = pr / a.group;
   float m = -INFINITY;
   auto slot = [&](int c) {
     return ws + (2 * c + (share_begin(total, grid, c) > u0 ? 0 : 1)) * slot_floats;
@@ -361,8 +363,6 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
     o[2] = fmaf(v.z, f, o[2]);
     o[3] = fmaf(v.w, f, o[3]);
   }
-  uint32_t mask[4];
-  node_mask(a, b, node, mask);
   const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) && l != 0.f;
   T *out = static_cast<T *>(a.out.data) +
            at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);

@@ -1,0 +1,867 @@
+// Dense attention on the tensor cores (tcgen05): bf16 and fp16, head_dim up to 128.
+//
+// Mathematics: one pass over the keys in tiles of 128. Per row, with x = scale log2(e) q.k,
+//   S = Q K^T;  m: reference maximum;  P = 2^(x - m + bias);  l += sum P;  O += P V;  out = O / l.
+// m only moves when a row's maximum exceeds it by more than 8 (a factor 2^8 in P, harmless in the
+// float32 sums): then l and O are multiplied by 2^(m - m'). P enters the second product in the
+// element type (half a step of relative rounding per weight, as the output's own); bias is 0 for
+// bf16 and 6 for fp16, which moves fp16's subnormal range from 2^-14 to 2^-20 of the largest
+// weight. l sums the unrounded float32 values. S, m, l and O are float32.
+//
+// What bounds it: per SM and tile of 128 x 128 pairs at head_dim 128, 1,024 clocks of tensor core
+// (4,096 multiply-adds a clock) and 1,024 clocks of the exponential unit (16 a clock), so both have
+// to run all the time: two independent streams per CTA, each with its own S and O in tensor
+// memory, alternate between the tensor core and their own softmax warpgroup. Long caches with few
+// rows are bound by HBM instead (the keys and values cross once).
+//
+// Streams: MODE_PROMPT and MODE_ROWS give each stream its own 128 rows over the same key tiles;
+// MODE_KEYS (a tree of at most 128 packed rows) gives both the same rows and every other tile, and
+// adds the two results up at the end.
+//
+// Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row; P goes back to tensor memory in S's
+// place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring;
+// 9 issues the MMAs; 10-11 look through value tiles of which some row must not see some key, and
+// replace what is not finite by zero before the MMA reads it (0 * NaN would reach every row); if
+// such a value is seen by some row, the epilogue adds it to exactly the rows that see it.
+//
+// Tensor memory (512 columns): S0, S1 at 0 and 128 (P over their first 64), O0, O1 at 256.
+#include "dense.cuh"
+#include "profiling.h"
+#include "tc_sm100.cuh"
+
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+namespace iskv {
+namespace {
+
+using namespace dense;
+using namespace tc;
+
+constexpr int KT = 128;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr uint64_t WAIT_NS = 2000000000ull;
+constexpr float LAZY = 8.f;  // log2 of the growth of a row's maximum that is left in P
+enum { MODE_PROMPT = 0, MODE_ROWS = 1, MODE_KEYS = 2 };
+constexpr int MAX_SLOTS = 8;
+
+struct Maps {
+  CUtensorMap k, v, kc, vc;  // kc, vc: tree
+  // 0: the axis has stride 0 or length one, every index reads its one element
+  int32_t k_head, v_head, kc_head, vc_head, k_batch, v_batch, kc_batch, vc_batch;
+};
+
+struct Ctl {
+  uint64_t kv_full[MAX_SLOTS], kv_empty[MAX_SLOTS];
+  // A value tile that needs the check: the loader has issued it (until then the parity of kv_full
+  // says nothing about it), the check has passed it. A phase each per checked use of the slot, which
+  // is not refilled before the MMA has read it.
+  uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t both, drain;
+  uint32_t tmem;
+  int abort;
+  int fix[8];              // unit number whose masked value tiles held something not finite
+};
+
+template <int HD, int MODE>
+struct Cfg {
+  static constexpr int SLABS = HD / 64;
+  static constexpr int TILE = KT * HD * 2;                  // bytes of 128 rows
+  static constexpr int NQ = MODE == MODE_KEYS ? 1 : 2;
+  static constexpr int ROWS = 128 * NQ;                     // packed rows of a unit
+  static constexpr int AHEAD = MODE == MODE_KEYS ? 2 : 1;   // key tiles ahead of the value tile
+  // As many ring slots as fit beside the query tiles in 227 KB, at most 8.
+  static constexpr int FIT = (232448 - 1024 - (int)sizeof(Ctl) - NQ * TILE) / TILE;
+  static constexpr int SLOTS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
+  static constexpr int SMEM = 1024 + NQ * TILE + SLOTS * TILE + (int)sizeof(Ctl);
+};
+
+ISKV_DEV void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
+                          uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+      : "memory");
+}
+
+ISKV_DEV void tmem_ld32(uint32_t taddr, float *v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
+      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+ISKV_DEV void tmem_st32(uint32_t taddr, const float *v) {
+  uint32_t r[16];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
+    tmem_st16(taddr + 16 * h, r);
+  }
+}
+
+ISKV_DEV float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Two float32 at once (the packed FMA and add of sm_100).
+ISKV_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+ISKV_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+template <typename T>
+ISKV_DEV uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same<T, __half>::value) {
+    __half2 h = __floats2half2_rn(a, b);
+    return *reinterpret_cast<uint32_t *>(&h);
+  } else {
+    return pack_bf16(a, b);
+  }
+}
+
+// Bits of the exponent of two packed elements; all set: not finite.
+template <typename T>
+constexpr uint32_t EXP_BITS = std::is_same<T, __half>::value ? 0x7C007C00u : 0x7F807F80u;
+
+template <typename T>
+ISKV_DEV bool finite_bits(T x) {
+  const uint32_t e = EXP_BITS<T> & 0xffffu;
+  return (*reinterpret_cast<const uint16_t *>(&x) & e) != e;
+}
+
+// kind::f16 instruction descriptor: float32 accumulator, A and B of type T, A K-major; b_mn: B is
+// MN-major.
+template <typename T>
+__host__ __device__ constexpr uint32_t idesc(int M, int N, bool b_mn) {
+  return (1u << 4) | (std::is_same<T, __half>::value ? 0u : (1u << 7) | (1u << 10)) |
+         (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+ISKV_DEV int64_t at(const iskv_heads &x, int64_t b, int64_t row, int64_t head) {
+  return b * x.batch + row * x.row + head * x.head;
+}
+
+// The CTA's units in order, the same for every warp (whole-warp calls).
+template <int MODE, int ROWS>
+struct Walk {
+  int64_t x = 0, end = 0;
+  int count = 0;  // units handed out so far
+
+  ISKV_DEV void begin(const DenseArgs &a) {
+    if constexpr (MODE != MODE_PROMPT) {
+      const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
+      const int64_t total = total_tiles<KT>(a, blocks);
+      x = share_begin(total, gridDim.x, blockIdx.x);
+      end = share_begin(total, gridDim.x, blockIdx.x + 1);
+    }
+  }
+  ISKV_DEV bool next(const DenseArgs &a, Unit &u) {
+    if constexpr (MODE == MODE_PROMPT) {
+      if (count++) return false;
+      if (!find_prompt_unit<ROWS>(a, blockIdx.x / a.n_kv, u)) return false;
+      u.kvh = blockIdx.x % a.n_kv;
+      u.t0 = 0;
+      u.t1 = u.n_tiles = last_token(a, u) / KT + 1;
+      u.cache_tiles = 0;
+      return true;
+    } else {
+      if (x >= end) return false;
+      const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
+      int64_t start;
+      const int b = find_entry<KT>(a, blocks, x, start);
+      if (b < 0) return false;
+      tree_unit<ROWS, KT>(a, b, start, x, end, u);
+      x += u.t1 - u.t0;
+      ++count;
+      return true;
+    }
+  }
+};
+
+// Tiles that stream s takes of the unit.
+template <int MODE>
+ISKV_DEV int stream_tiles(const DenseArgs &a, const Unit &u, int s) {
+  const int n = u.t1 - u.t0;
+  if (MODE == MODE_KEYS) return (n + 1 - s) / 2;
+  if (u.n_rows <= 128 * s) return 0;
+  if (MODE == MODE_ROWS) return n;
+  return (u.row0 + min(u.n_rows, 128 * (s + 1)) - 1) / a.group / KT + 1;
+}
+
+// Rows [r0, r1) of value tile t that some row of the unit must not see; false: none.
+template <int MODE>
+ISKV_DEV bool hidden_rows(const DenseArgs &a, const Unit &u, int t, int &r0, int &r1) {
+  r1 = KT;
+  if (MODE == MODE_PROMPT) {
+    r0 = max(0, first_token(a, u) + 1 - t * KT);
+  } else if (t < u.cache_tiles) {
+    r0 = u.len - t * KT;
+  } else {
+    r0 = 0;
+    r1 = a.nodes;
+  }
+  return r0 < r1;
+}
+
+template <typename T, int HD, int MODE>
+__global__ void __launch_bounds__(384, 1)
+    k_dense_tc(const __grid_constant__ DenseArgs a, const __grid_constant__ Maps maps) {
+  using C = Cfg<HD, MODE>;
+  constexpr bool TREE = MODE != MODE_PROMPT;
+  extern __shared__ char raw[];
+  char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  Ctl &ctl = *reinterpret_cast<Ctl *>(base + (C::NQ + C::SLOTS) * C::TILE);
+  const uint32_t q_smem = smem_u32(base), ring_smem = q_smem + C::NQ * C::TILE;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  volatile int *abort = &ctl.abort;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(&ctl.kv_full[i], 1);
+      mbar_init(&ctl.kv_empty[i], 1);
+      mbar_init(&ctl.v_req[i], 1);
+      mbar_init(&ctl.v_ok[i], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl.q_full[i], MODE == MODE_KEYS ? 8 : 4);
+      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.p_full[i], 4);
+      mbar_init(&ctl.o_full[i], 1);
+    }
+    mbar_init(&ctl.both, 8);
+    mbar_init(&ctl.drain, 1);
+    ctl.abort = 0;
+    for (int i = 0; i < 8; ++i) ctl.fix[i] = 0;
+    fence_barrier_init();
+  }
+  if (warp == 9) tmem_alloc(&ctl.tmem, 512);
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl.tmem;
+  constexpr uint32_t O_COL = 256;
+
+  Walk<MODE, C::ROWS> walk;
+  Unit u;
+  walk.begin(a);
+
+  // Registers: 256 x 208 + 128 x 88 = 64,512, the launch's 384 x 168.
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    // ------------------------------------------------------------------------- softmax
+    const int st = warp / 4, tid = threadIdx.x & 127;  // stream; row of its tile
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane base of the warp
+    const uint32_t s_tm = tmem + lanes + 128 * st, o_tm = tmem + lanes + O_COL + HD * st;
+    const float c = fmaxf(fabsf(a.scale) * LOG2E, 1e-30f);
+    constexpr float BIAS = std::is_same<T, __half>::value ? 6.f : 0.f;
+    char *q_tile = base + (MODE == MODE_KEYS ? 0 : st) * C::TILE;
+    const int row_off = MODE == MODE_KEYS ? 0 : 128 * st;  // first unit row of the tile
+    uint32_t ph_s = 0, ph_o = 0, ph_both = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t &ph) {
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, ph, abort, WAIT_NS));
+      if (!ok) ctl.abort = 1;
+      ph ^= 1;
+      return ok;
+    };
+    // Both warpgroups have come here.
+    auto meet = [&]() {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl.both);
+      return wait(&ctl.both, ph_both);
+    };
+
+    while (ok && walk.next(a, u)) {
+      const int n_mine = stream_tiles<MODE>(a, u, st);
+      const int tile_rows = u.n_rows - row_off;  // rows of this stream's tile, may exceed 128
+      const int64_t row_base = TREE ? 0 : u.base;
+      const int entry = TREE ? u.b : 0;
+
+      // Queries into shared memory: K-major, 128-byte swizzle; the scale's sign goes with them. (A
+      // stream without tiles skips the unit, so that it cannot run ahead of the MMA warp.)
+      if (MODE == MODE_KEYS || n_mine > 0) {
+        constexpr int CH = HD / 8;
+        const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+        const T *q = static_cast<const T *>(a.q.data);
+        // Every warp its own 32 rows (in MODE_KEYS half of their columns).
+        constexpr int CW = MODE == MODE_KEYS ? CH / 2 : CH;
+#pragma unroll 8
+        for (int i = lane; i < 32 * CW; i += 32) {
+          const int r = (warp & 3) * 32 + i / CW;
+          const int ch = i % CW + (MODE == MODE_KEYS ? st * CW : 0);
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (r < tile_rows && ch * 8 < a.head_dim) {
+            const int pr = u.row0 + row_off + r;
+            x = *reinterpret_cast<const uint4 *>(
+                q + at(a.q, entry, row_base + pr / a.group,
+                       (int64_t)u.kvh * a.group + pr % a.group) + ch * 8);
+            x.x ^= flip;
+            x.y ^= flip;
+            x.z ^= flip;
+            x.w ^= flip;
+          }
+          *reinterpret_cast<uint4 *>(q_tile + (ch / 8) * 16384 + r * 128 +
+                                     (((ch & 7) ^ (r & 7)) * 16)) = x;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.q_full[MODE == MODE_KEYS ? 0 : st]);
+      }
+
+      const int my_row = min(tid, tile_rows - 1);
+      const int pr = u.row0 + row_off + max(my_row, 0);
+      const int tok = pr / a.group;  // prompt: the row's token; tree: its node
+      const bool busy = (warp & 3) * 32 < tile_rows;  // the warp has a row
+      uint32_t mask[4] = {0, 0, 0, 0};
+      if constexpr (TREE) {
+        if (busy) node_mask(a, a.parents + (int64_t)u.b * a.nodes, tok, mask);
+      }
+
+      float m = -INFINITY, l = 0.f;
+      for (int i = 0; ok && i < n_mine; ++i) {
+        const int t = u.t0 + (MODE == MODE_KEYS ? 2 * i + st : i);
+        if (!wait(&ctl.s_full[st], ph_s)) break;
+        fence_after_sync();
+        if (busy) {
+          float s[128];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
+          tmem_ld_wait();
+          int r0, r1;
+          if (hidden_rows<MODE>(a, u, t, r0, r1)) {
+            if (!TREE || t < u.cache_tiles) {
+              const int lim = TREE ? u.len - 1 - t * KT : tok - t * KT;  // last visible column
+#pragma unroll
+              for (int j = 0; j < 128; ++j) s[j] = j <= lim ? s[j] : -INFINITY;
+            } else {
+#pragma unroll
+              for (int j = 0; j < 128; ++j)
+                s[j] = mask[j / 32] >> (j % 32) & 1 ? s[j] : -INFINITY;
+            }
+          }
+          float top[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) top[j] = s[j];
+#pragma unroll
+          for (int j = 4; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
+          const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          const bool grow = mn > m && (m == -INFINITY || (mn - m) * c > LAZY);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+            l *= f;
+            m = mn;
+            // S(i) complete: so is the previous P V of this stream, which was issued before it
+            if (i > 0) {
+#pragma unroll
+              for (int j = 0; j < HD / 32; ++j) {
+                float o[32];
+                tmem_ld32(o_tm + 32 * j, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] *= f;
+                tmem_st32(o_tm + 32 * j, o);
+              }
+            }
+          }
+          const float off = BIAS - (m == -INFINITY ? 0.f : m * c);
+          const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t p[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float2 x = fma2(make_float2(s[32 * j + 2 * e], s[32 * j + 2 * e + 1]), c2, off2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum[e & 1] = add2(sum[e & 1], x);
+              p[e] = pack2<T>(x.x, x.y);
+            }
+            tmem_st16(s_tm + 16 * j, p);
+          }
+          l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
+          tmem_st_wait();
+        }
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[st]);
+      }
+      if (!ok) break;
+
+      // Epilogue.
+      if (n_mine > 0 && !wait(&ctl.o_full[st], ph_o)) break;
+      float w[2] = {0.f, 0.f};  // weights of the two streams' O
+      int c0 = 0, c1 = HD;      // this thread's columns
+      float ml = m == -INFINITY ? -INFINITY : m * c;
+      if constexpr (MODE == MODE_KEYS) {
+        // The query tile is idle once both streams' products are complete.
+        if (!meet()) break;
+        float *stat = reinterpret_cast<float *>(base);
+        stat[(2 * st) * 128 + tid] = ml;
+        stat[(2 * st + 1) * 128 + tid] = l;
+        if (!meet()) break;
+        const float m0 = stat[tid], l0 = stat[128 + tid], m1 = stat[256 + tid],
+                    l1 = stat[384 + tid];
+        if (!meet()) break;  // the statistics' place is free again
+        ml = fmaxf(m0, m1);
+        const float ref = ml == -INFINITY ? 0.f : ml;
+        w[0] = ex2(m0 - ref);
+        w[1] = ex2(m1 - ref);
+        l = l0 * w[0] + (stream_tiles<MODE>(a, u, 1) > 0 ? l1 * w[1] : 0.f);
+        c0 = HD / 2 * st;
+        c1 = c0 + HD / 2;
+      }
+      fence_after_sync();
+      const bool two = MODE == MODE_KEYS && stream_tiles<MODE>(a, u, 1) > 0;
+      const bool fix = *(volatile int *)&ctl.fix[walk.count & 7] == walk.count;
+      const bool whole = !TREE || (u.t0 == 0 && u.t1 == u.n_tiles);
+      const bool mine = tid < tile_rows;
+      const bool live = !TREE || (mask[0] | mask[1] | mask[2] | mask[3]);
+      if (busy) {
+        const uint32_t o0 = tmem + lanes + O_COL;
+        const float inv = 1.f / l;
+        const bool zero = l == 0.f || !live;
+        char *stage = q_tile + (size_t)tid * HD * 2;
+        float *slot = static_cast<float *>(a.ws) +
+                      (2 * blockIdx.x + (u.t0 > 0 ? 0 : 1)) * dense_slot_floats(C::ROWS, HD);
+#pragma unroll 1
+        for (int col = c0; col < c1; col += 32) {
+          float o[32];
+          if constexpr (MODE == MODE_KEYS) {
+            float o1[32];
+            tmem_ld32(o0 + col, o);
+            tmem_ld32(o0 + HD + col, o1);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = two ? o[e] * w[0] + o1[e] * w[1] : o[e] * w[0];
+          } else {
+            tmem_ld32(o_tm + col, o);
+            tmem_ld_wait();
+          }
+          if (fix && mine) {
+            // Values that were replaced by zero, for the rows that see them.
+            const int lo = TREE ? 0 : first_token(a, u) + 1, hi = TREE ? a.nodes : tok + 1;
+            if (!TREE || u.t1 > u.cache_tiles) {
+              const T *v = static_cast<const T *>(a.v.data) + at(a.v, entry, row_base, u.kvh);
+              for (int j = lo; j < hi; ++j) {
+                if (TREE && !((j < 64 ? j < 32 ? mask[0] : mask[1] : j < 96 ? mask[2] : mask[3]) >>
+                              (j & 31) & 1))
+                  continue;
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                  if (col + e >= a.head_dim) break;
+                  const T x = v[j * a.v.row + col + e];
+                  if (!finite_bits(x)) o[e] += to_f(x);
+                }
+              }
+            }
+          }
+          if (whole) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = zero ? 0.f : o[e] * inv;
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              const int ch = col / 8 + q4;
+              *reinterpret_cast<uint4 *>(stage + ((ch ^ (tid & 7)) * 16)) = make_uint4(
+                  pack2<T>(o[8 * q4], o[8 * q4 + 1]), pack2<T>(o[8 * q4 + 2], o[8 * q4 + 3]),
+                  pack2<T>(o[8 * q4 + 4], o[8 * q4 + 5]), pack2<T>(o[8 * q4 + 6], o[8 * q4 + 7]));
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int q4 = 0; q4 < 8; ++q4)
+              reinterpret_cast<float4 *>(slot)[(size_t)(col / 4 + q4) * C::ROWS + row_off + tid] =
+                  make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+          }
+        }
+        if (!whole) {
+          if (mine && (MODE != MODE_KEYS || st == 0)) {
+            slot[(size_t)C::ROWS * HD + row_off + tid] = ml;
+            slot[(size_t)C::ROWS * (HD + 1) + row_off + tid] = l;
+          }
+        } else {
+          // Whole rows leave in coalesced 16-byte pieces, the warp's own 32 rows.
+          __syncwarp();
+          T *out = static_cast<T *>(a.out.data) +
+                   at(a.out, entry, row_base + pr / a.group,
+                      (int64_t)u.kvh * a.group + pr % a.group);
+          const int n_rows = min(32, tile_rows - (warp & 3) * 32);
+          const int ch0 = c0 / 8, chn = (c1 - c0) / 8;
+#pragma unroll 4
+          for (int i = lane; i < 32 * chn; i += 32) {
+            const int r = i / chn, ch = ch0 + i % chn;
+            T *dst = reinterpret_cast<T *>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r));
+            const int rr = (warp & 3) * 32 + r;
+            if (r < n_rows && ch * 8 < a.head_dim)
+              *reinterpret_cast<uint4 *>(dst + ch * 8) = *reinterpret_cast<const uint4 *>(
+                  q_tile + (size_t)rr * HD * 2 + ((ch ^ (rr & 7)) * 16));
+          }
+        }
+      }
+      fence_before_sync();
+      // The query tile and both O are read by both warpgroups: neither goes on before the other.
+      if constexpr (MODE == MODE_KEYS) {
+        if (!meet()) break;
+        fence_after_sync();
+      }
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  if (warp == 8) {
+    // ------------------------------------------------------------------------- loads
+    RingPos pos;
+    int issued = 0;
+    bool ok = true;
+    while (ok && walk.next(a, u)) {
+      if (lane == 0) {
+        const int n = u.t1 - u.t0;
+        auto load = [&](int t, bool value) {
+          if (!ok) return;
+          if (!mbar_wait(&ctl.kv_empty[pos.slot], pos.phase ^ 1, abort, WAIT_NS)) {
+            ok = false;
+            ctl.abort = 1;
+            return;
+          }
+          const bool cache = TREE && t < u.cache_tiles;
+          const CUtensorMap *map = cache ? (value ? &maps.vc : &maps.kc) : (value ? &maps.v : &maps.k);
+          const int head = u.kvh * (cache ? (value ? maps.vc_head : maps.kc_head)
+                                          : (value ? maps.v_head : maps.k_head));
+          const int entry = TREE ? u.b * (cache ? (value ? maps.vc_batch : maps.kc_batch)
+                                                : (value ? maps.v_batch : maps.k_batch))
+                                 : 0;
+          const int row = TREE ? (cache ? t : t - u.cache_tiles) * KT : (int)u.base + t * KT;
+          const uint32_t dst = ring_smem + pos.slot * C::TILE;
+          mbar_arrive_expect_tx(&ctl.kv_full[pos.slot], C::TILE);
+          int r0, r1;
+          if (value && hidden_rows<MODE>(a, u, t, r0, r1)) mbar_arrive(&ctl.v_req[pos.slot]);
+          for (int s = 0; s < C::SLABS; ++s)
+            tma_load_4d(dst + s * 16384, map, s * 64, head, row, entry, &ctl.kv_full[pos.slot]);
+          ++issued;
+          pos.next(C::SLOTS);
+        };
+        for (int i = 0; i < C::AHEAD && i < n; ++i) load(u.t0 + i, false);
+        for (int i = 0; i < n; ++i) {
+          load(u.t0 + i, true);
+          if (i + C::AHEAD < n) load(u.t0 + i + C::AHEAD, false);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+    }
+    if (lane == 0) {
+      // Copies in flight land before the CTA ends (after a timeout nobody else waits for them): the
+      // last use of every slot that was issued.
+      RingPos p;
+      for (int i = 0; i < issued; ++i) {
+        if (i + C::SLOTS >= issued) {
+          const uint64_t t0 = globaltimer();
+          while (!mbar_try_wait(&ctl.kv_full[p.slot], p.phase) && globaltimer() - t0 < WAIT_NS) {
+          }
+        }
+        p.next(C::SLOTS);
+      }
+    }
+  } else if (warp == 9) {
+    // ------------------------------------------------------------------------- MMAs
+    constexpr uint32_t ID_S = idesc<T>(128, KT, false), ID_O = idesc<T>(128, HD, true);
+    RingPos pos;
+    uint32_t ph_q[2] = {0, 0}, ph_v = 0, ph_p[2] = {0, 0};  // ph_v: a bit per slot
+    bool ok = true;
+    auto wait = [&](uint64_t *bar, uint32_t ph) {
+      if (ok && !mbar_wait(bar, ph, abort, WAIT_NS)) {
+        ok = false;
+        ctl.abort = 1;
+      }
+      return ok;
+    };
+    auto scores = [&](int s, uint32_t k_tile) {
+      const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : s) * C::TILE);
+      const uint64_t kd = sw128_desc(k_tile);
+#pragma unroll
+      for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+        mma_bf16(tmem + 128 * s, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
+      }
+      mma_commit(&ctl.s_full[s]);
+    };
+    auto values = [&](int s, uint32_t v_tile, bool first) {
+      const uint64_t vd = sw128_mn_desc(v_tile, 16384);
+#pragma unroll
+      for (int k = 0; k < KT / 16; ++k)
+        mma_bf16_ts(tmem + O_COL + HD * s, tmem + 128 * s + 8 * k, desc_add(vd, k * 2048), ID_O,
+                    !first || k > 0);
+    };
+    while (ok && walk.next(a, u)) {
+      if (lane == 0) {
+        const int n = u.t1 - u.t0;
+        const int n_s[2] = {stream_tiles<MODE>(a, u, 0), stream_tiles<MODE>(a, u, 1)};
+        auto tile_at = [&](const RingPos &p) { return ring_smem + p.slot * C::TILE; };
+        for (int s = 0; s < (MODE == MODE_KEYS ? 1 : 2); ++s)
+          if (n_s[s] > 0) {
+            wait(&ctl.q_full[s], ph_q[s]);
+            ph_q[s] ^= 1;
+          }
+        for (int i = 0; i < C::AHEAD && i < n && ok; ++i) {
+          if (!wait(&ctl.kv_full[pos.slot], pos.phase)) break;
+          fence_after_sync();
+          for (int s = 0; s < 2; ++s)
+            if (MODE == MODE_KEYS ? s == i : n_s[s] > 0) scores(s, tile_at(pos));
+          mma_commit(&ctl.kv_empty[pos.slot]);
+          pos.next(C::SLOTS);
+        }
+        for (int i = 0; i < n && ok; ++i) {
+          const RingPos vp = pos;
+          pos.next(C::SLOTS);
+          const bool more = i + C::AHEAD < n;
+          const RingPos kp = pos;
+          if (more) pos.next(C::SLOTS);
+          if (!wait(&ctl.kv_full[vp.slot], vp.phase)) break;
+          int r0, r1;
+          if (hidden_rows<MODE>(a, u, u.t0 + i, r0, r1)) {
+            if (!wait(&ctl.v_ok[vp.slot], ph_v >> vp.slot & 1)) break;
+            ph_v ^= 1u << vp.slot;
+          }
+          bool have_k = false;
+          for (int s = 0; s < 2; ++s) {
+            const int mine = MODE == MODE_KEYS ? i / 2 : i;  // the stream's tile number
+            if (MODE == MODE_KEYS ? (i & 1) != s : i >= n_s[s]) continue;
+            if (!wait(&ctl.p_full[s], ph_p[s])) break;
+            ph_p[s] ^= 1;
+            fence_after_sync();
+            values(s, tile_at(vp), mine == 0);
+            if (mine == n_s[s] - 1) mma_commit(&ctl.o_full[s]);
+            if (MODE == MODE_KEYS) mma_commit(&ctl.kv_empty[vp.slot]);
+            if (mine + 1 < n_s[s]) {
+              if (!have_k && !wait(&ctl.kv_full[kp.slot], kp.phase)) break;
+              have_k = true;
+              fence_after_sync();
+              scores(s, tile_at(kp));
+            }
+          }
+          if (!ok) break;
+          if (MODE != MODE_KEYS) mma_commit(&ctl.kv_empty[vp.slot]);
+          if (more) mma_commit(&ctl.kv_empty[kp.slot]);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+    }
+    // Every MMA and commit has completed before the CTA gives its tensor memory back.
+    if (lane == 0) {
+      mma_commit(&ctl.drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&ctl.drain, 0) && globaltimer() - t0 < WAIT_NS) {
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------------------- value check
+    RingPos pos;
+    uint32_t ph_req = 0;  // a bit per slot
+    bool ok = true;
+    while (ok && walk.next(a, u)) {
+      const int n = u.t1 - u.t0;
+      for (int i = 0; i < C::AHEAD && i < n; ++i) pos.next(C::SLOTS);
+      for (int i = 0; i < n && ok; ++i) {
+        const int t = u.t0 + i;
+        int r0, r1;
+        if (hidden_rows<MODE>(a, u, t, r0, r1)) {
+          ok = __all_sync(0xffffffffu,
+                          mbar_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort, WAIT_NS) &&
+                              mbar_wait(&ctl.kv_full[pos.slot], pos.phase, abort, WAIT_NS));
+          ph_req ^= 1u << pos.slot;
+          if (!ok) {
+            ctl.abort = 1;
+            break;
+          }
+          // A row is 8 16-byte pieces of each 64-column slab, whatever their swizzled order.
+          char *tile = base + (C::NQ + pos.slot) * C::TILE;
+          const int half = warp - 10, pieces = (r1 - r0) * 8;
+          const int p0 = r0 * 8 + half * pieces / 2, p1 = r0 * 8 + (half + 1) * pieces / 2;
+          uint32_t top = 0;
+          for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll 4
+            for (int p = p0 + lane; p < p1; p += 32) {
+              const uint4 x = *reinterpret_cast<const uint4 *>(tile + s * 16384 + p * 16);
+              top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+            }
+          constexpr uint32_t E = EXP_BITS<T> & 0xffffu;
+          if (__any_sync(0xffffffffu, (top & 0xffffu) >= E || (top >> 16) >= E)) {
+            // Cache rows beyond the valid ones, and rows behind a sequence, are seen by nobody.
+            const int seen_end = TREE ? (t < u.cache_tiles ? 0 : a.nodes) : u.len - t * KT;
+            bool seen = false;
+            for (int s = 0; s < C::SLABS; ++s)
+              for (int p = p0 + lane; p < p1; p += 32) {
+                uint4 *at16 = reinterpret_cast<uint4 *>(tile + s * 16384 + p * 16);
+                uint4 x = *at16;
+                uint32_t *wd = reinterpret_cast<uint32_t *>(&x);
+                bool hit = false;
+                for (int e = 0; e < 4; ++e) {
+                  if ((wd[e] & E) == E) {
+                    wd[e] &= 0xffff0000u;
+                    hit = true;
+                  }
+                  if ((wd[e] >> 16 & E) == E) {
+                    wd[e] &= 0xffffu;
+                    hit = true;
+                  }
+                }
+                if (hit) {
+                  *at16 = x;
+                  seen |= p / 8 < seen_end;
+                }
+              }
+            if (__any_sync(0xffffffffu, seen) && lane == 0)
+              *(volatile int *)&ctl.fix[walk.count & 7] = walk.count;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.v_ok[pos.slot]);
+        }
+        pos.next(C::SLOTS);
+        if (i + C::AHEAD < n) pos.next(C::SLOTS);
+      }
+    }
+  }
+  }
+
+  __syncwarp();
+  fence_before_sync();
+  __syncthreads();
+  if (threadIdx.x == 0 && ctl.abort) report(a.status, ISKV_ERR_TIMEOUT);
+  if (warp == 9) {
+    fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------------------------------------
+// Host
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void *f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
+            cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  });
+  return fn;
+}
+
+// Two-byte rows as a 4-D tensor {head_dim, heads, rows, entries}, box {64, 1, 128, 1}, 128-byte
+// swizzle; what lies outside reads as zero.
+bool encode(CUtensorMap *m, int32_t &head_on, int32_t &batch_on, const iskv_heads &x, int hd,
+            int heads, int64_t rows, int64_t entries, int dtype) {
+  head_on = heads > 1 && x.head > 0;
+  batch_on = entries > 1 && x.batch > 0;
+  // Axes that are not walked get length one and any legal stride.
+  const cuuint64_t any = (cuuint64_t)(hd + 7) / 8 * 16;
+  cuuint64_t dims[4] = {(cuuint64_t)hd, head_on ? (cuuint64_t)heads : 1, (cuuint64_t)rows,
+                        batch_on ? (cuuint64_t)entries : 1};
+  cuuint64_t strides[3] = {head_on ? (cuuint64_t)x.head * 2 : any,
+                           x.row > 0 ? (cuuint64_t)x.row * 2 : any,
+                           batch_on ? (cuuint64_t)x.batch * 2 : any};
+  cuuint32_t box[4] = {64, 1, KT, 1}, one[4] = {1, 1, 1, 1};
+  return encode_fn()(m, dtype == ISKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                     4, x.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T, int HD, int MODE>
+cudaError_t run(const DenseArgs &a, const Maps &maps, int grid, cudaStream_t s) {
+  auto *kernel = k_dense_tc<T, HD, MODE>;
+  constexpr int smem = Cfg<HD, MODE>::SMEM;
+  static_assert(smem <= 232448 && Cfg<HD, MODE>::SLOTS >= 4, "ring does not fit");
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, 384, smem, s>>>(a, maps);
+  count_launches(1);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+bool dense_tc_takes(const DenseArgs &a) {
+  if (a.dtype == ISKV_F32 || a.head_dim % 8 || a.head_dim > 128 || !encode_fn()) return false;
+  auto fits = [&](const iskv_heads &x, bool rows_walked) {
+    return reinterpret_cast<uintptr_t>(x.data) % 16 == 0 && x.row % 8 == 0 && x.head % 8 == 0 &&
+           (!a.tree || x.batch % 8 == 0) && (x.row > 0 || !rows_walked);
+  };
+  const int64_t n = a.tree ? a.nodes : a.rows;
+  return fits(a.q, false) && fits(a.out, false) && fits(a.k, n > 1) && fits(a.v, n > 1) &&
+         (!a.tree || a.rows == 0 || (fits(a.kc, a.rows > 1) && fits(a.vc, a.rows > 1)));
+}
+
+bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e) {
+  Maps maps = {};
+  const int64_t n = a.tree ? a.nodes : a.rows, entries = a.tree ? a.batch : 1;
+  bool ok = encode(&maps.k, maps.k_head, maps.k_batch, a.k, a.head_dim, a.n_kv, n, entries, a.dtype) &&
+            encode(&maps.v, maps.v_head, maps.v_batch, a.v, a.head_dim, a.n_kv, n, entries, a.dtype);
+  if (a.tree && a.rows > 0)
+    ok = ok &&
+         encode(&maps.kc, maps.kc_head, maps.kc_batch, a.kc, a.head_dim, a.n_kv, a.rows, entries,
+                a.dtype) &&
+         encode(&maps.vc, maps.vc_head, maps.vc_batch, a.vc, a.head_dim, a.n_kv, a.rows, entries,
+                a.dtype);
+  if (!ok) return false;
+  const bool keys = a.tree && a.nodes * a.group <= 128;
+  const int rows = keys ? 128 : 256;
+  const int64_t grid = a.tree ? DENSE_TC_GRID : (a.rows * a.group / rows + a.batch) * (int64_t)a.n_kv;
+  if (grid > 0x7fffffff) {
+    e = cudaErrorInvalidValue;
+    return true;
+  }
+  auto width = [&](auto tag, auto hd) {
+    using T = decltype(tag);
+    constexpr int HD = decltype(hd)::value;
+    e = !a.tree ? run<T, HD, MODE_PROMPT>(a, maps, (int)grid, s)
+        : keys  ? run<T, HD, MODE_KEYS>(a, maps, (int)grid, s)
+                : run<T, HD, MODE_ROWS>(a, maps, (int)grid, s);
+  };
+  auto type = [&](auto tag) {
+    if (a.head_dim <= 64) width(tag, std::integral_constant<int, 64>{});
+    else width(tag, std::integral_constant<int, 128>{});
+  };
+  if (a.dtype == ISKV_F16) type(__half{});
+  else type(__nv_bfloat16{});
+  if (e == cudaSuccess && a.tree) e = launch_dense_join(a, (int)grid, rows, KT, s);
+  return true;
+}
+
+}  // namespace iskv

@@ -348,6 +348,14 @@ def test_tree_padding(dtype, group):
 
 
 @pytest.mark.parametrize("dtype", DT)
+def test_tree_last_row_block_is_short(dtype):
+    """300 packed rows: row blocks of 256 and 44, the second without work for half of the kernel;
+    more units than CTAs, so that a CTA meets both kinds in turn."""
+    run_tree(12, dtype, 100, [5, 0, 260, 131, 40, 77, 10, 1] * 8, 3, 1, 64)
+    run_tree(13, dtype, 100, [300, 1], 12, 4, 64)
+
+
+@pytest.mark.parametrize("dtype", DT)
 def test_tree_scales(dtype):
     run_tree(6, dtype, 6, [700], 4, 1, 64, scale=-0.2)
     run_tree(7, dtype, 6, [700], 4, 1, 64, scale=0.0)
