@@ -59,6 +59,15 @@ ISKV_DEV int seq_len(const DenseArgs &a, int s, int64_t &lo) {
 template <int ROWS>
 ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   const int lane = threadIdx.x & 31;
+  if (a.batch == 1) {
+    u.b = 0;
+    u.len = seq_len(a, 0, u.base);
+    const int n = (int)(((int64_t)u.len * a.group + ROWS - 1) / ROWS);
+    if (rank >= n) return false;
+    u.row0 = (n - 1 - rank) * ROWS;
+    u.n_rows = min(ROWS, u.len * a.group - u.row0);
+    return true;
+  }
   auto blocks = [&](int s) {
     int64_t lo;
     return s < a.batch ? (int)(((int64_t)seq_len(a, s, lo) * a.group + ROWS - 1) / ROWS) : 0;
@@ -91,7 +100,9 @@ ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
       skip -= n;
       continue;
     }
-    u.b = s0 + (int)__fns(has, 0, skip + 1);
+    const unsigned pick = __ballot_sync(
+        0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == skip);
+    u.b = s0 + __ffs(pick) - 1;
     break;
   }
   u.len = seq_len(a, u.b, u.base);
@@ -116,71 +127,71 @@ ISKV_DEV int cached_rows(const DenseArgs &a, int b) {
   return n;
 }
 
-template <int KT>
-ISKV_DEV int64_t entry_tiles(const DenseArgs &a, int b, int blocks) {
-  return ((int64_t)(cached_rows(a, b) + KT - 1) / KT + (a.nodes + KT - 1) / KT) * a.n_kv * blocks;
-}
-
-// Whole warp: tiles of all entries.
-template <int KT>
-ISKV_DEV int64_t total_tiles(const DenseArgs &a, int blocks) {
-  int64_t n = 0;
-  for (int b = threadIdx.x & 31; b < a.batch; b += 32) n += entry_tiles<KT>(a, b, blocks);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-
-// Whole warp: the entry that holds tile x of the line, and the line position of its first tile.
-template <int KT>
-ISKV_DEV int find_entry(const DenseArgs &a, int blocks, int64_t x, int64_t &start) {
-  const int lane = threadIdx.x & 31;
-  int64_t before = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
-    const int64_t n = b0 + lane < a.batch ? entry_tiles<KT>(a, b0 + lane, blocks) : 0;
-    int64_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += t;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      start = before + __shfl_sync(0xffffffffu, sum - n, l);
-      return b0 + l;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
-  }
-  start = before;
-  return -1;
-}
-
-// The share of CTA c: line positions [share(c), share(c + 1)); and the CTA that holds position x.
-ISKV_DEV int64_t share_begin(int64_t total, int grid, int c) { return total * c / grid; }
-ISKV_DEV int share_owner(int64_t total, int grid, int64_t x) {
-  return (int)(((x + 1) * grid - 1) / total);
-}
-
-// The unit holding line position x of entry b (first tile at line position start), cut to the
-// share's end.
+// The line of a tree call's tiles and a CTA's way along its share of it (whole-warp calls). Shares are
+// `per` tiles each, the last ones may be empty.
 template <int ROWS, int KT>
-ISKV_DEV void tree_unit(const DenseArgs &a, int b, int64_t start, int64_t x, int64_t end, Unit &u) {
-  u.b = b;
-  u.base = 0;
-  u.len = cached_rows(a, b);
-  u.cache_tiles = (u.len + KT - 1) / KT;
-  u.n_tiles = u.cache_tiles + (a.nodes + KT - 1) / KT;
-  const int all_rows = a.nodes * a.group, blocks = (all_rows + ROWS - 1) / ROWS;
-  const int64_t off = x - start;
-  const int idx = (int)(off / u.n_tiles);
-  u.kvh = idx / blocks;
-  u.row0 = (idx % blocks) * ROWS;
-  u.n_rows = min(ROWS, all_rows - u.row0);
-  u.t0 = (int)(off - (int64_t)idx * u.n_tiles);
-  const int64_t left = end - x;
-  u.t1 = (int)min((int64_t)u.n_tiles, u.t0 + left);
-}
+struct TreeLine {
+  int blocks, draft_tiles;
+  int len0;         // cached rows of entry `lane`: the first 32 entries stay in registers
+  int64_t total, per, x, end;
+
+  ISKV_DEV int len_of(const DenseArgs &a, int b) const {  // lane-varying b
+    return b < 32 ? len0 : cached_rows(a, b);
+  }
+  ISKV_DEV int64_t entry_tiles(const DenseArgs &a, int b) const {
+    return b < a.batch ? (int64_t)((len_of(a, b) + KT - 1) / KT + draft_tiles) * (a.n_kv * blocks) : 0;
+  }
+  ISKV_DEV void begin(const DenseArgs &a, int grid, int cta) {
+    const int lane = threadIdx.x & 31;
+    blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
+    draft_tiles = (a.nodes + KT - 1) / KT;
+    len0 = lane < a.batch ? cached_rows(a, lane) : 0;
+    total = 0;
+    for (int b = lane; b < a.batch; b += 32) total += entry_tiles(a, b);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    per = (total + grid - 1) / grid;
+    x = min(total, per * cta);
+    end = min(total, x + per);
+  }
+  // The next unit of the share, or false.
+  ISKV_DEV bool next(const DenseArgs &a, Unit &u) {
+    if (x >= end) return false;
+    const int lane = threadIdx.x & 31;
+    int64_t before = 0;
+    for (int b0 = 0;; b0 += 32) {
+      const int64_t n = entry_tiles(a, b0 + lane);
+      int64_t sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        before += __shfl_sync(0xffffffffu, sum - n, l);
+        u.b = b0 + l;
+        u.len = __shfl_sync(0xffffffffu, len_of(a, b0 + lane), l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+    u.base = 0;
+    u.cache_tiles = (u.len + KT - 1) / KT;
+    u.n_tiles = u.cache_tiles + draft_tiles;
+    const int all_rows = a.nodes * a.group;
+    const int64_t off = x - before;
+    const int idx = off >> 31 ? (int)(off / u.n_tiles) : (int)off / u.n_tiles;
+    u.kvh = idx / blocks;
+    u.row0 = (idx - u.kvh * blocks) * ROWS;
+    u.n_rows = min(ROWS, all_rows - u.row0);
+    u.t0 = (int)(off - (int64_t)idx * u.n_tiles);
+    u.t1 = (int)min((int64_t)u.n_tiles, u.t0 + (end - x));
+    x += u.t1 - u.t0;
+    return true;
+  }
+};
 
 // Whole warp: bits of the nodes that each lane's node i sees, given its entry's parents: itself and
 // its ancestors. par[i] is the index of an earlier node, or -1 (a child of the last cached token); an

@@ -28,7 +28,6 @@ struct Smem {
   float p[ROWS][KT + 4];
   uint32_t mask[DENSE_MAX_NODES][4];
   Unit unit;
-  int64_t pos, end, total;
 };
 
 ISKV_DEV float ex2(float x) {
@@ -261,6 +260,7 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
 
 template <typename T, int HD, bool TREE, bool VEC>
 __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseArgs a) {
+  if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) char raw[];
   Smem<HD> &sm = *reinterpret_cast<Smem<HD> *>(raw);
   if constexpr (!TREE) {
@@ -278,23 +278,13 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
     const Unit u = sm.unit;
     if (u.b >= 0) run_unit<T, HD, false, VEC>(a, sm, u);
   } else {
-    const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
-    int64_t x = 0, end = 0, start = 0;
-    for (bool first = true;; first = false) {
+    TreeLine<ROWS, KT> line;
+    if (threadIdx.x < 32) line.begin(a, gridDim.x, blockIdx.x);
+    for (;;) {
       __syncthreads();  // the previous unit's place is no longer read
       if (threadIdx.x < 32) {
-        if (first) {
-          const int64_t total = total_tiles<KT>(a, blocks);
-          x = share_begin(total, gridDim.x, blockIdx.x);
-          end = share_begin(total, gridDim.x, blockIdx.x + 1);
-        }
         Unit u;
-        u.b = -1;
-        if (x < end) {
-          const int b = find_entry<KT>(a, blocks, x, start);
-          tree_unit<ROWS, KT>(a, b, start, x, end, u);
-          x += u.t1 - u.t0;
-        }
+        if (!line.next(a, u)) u.b = -1;
         if (threadIdx.x == 0) sm.unit = u;
       }
       __syncthreads();
@@ -305,70 +295,100 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
   }
 }
 
-// One warp: 32 rows of one four-column group of one unit; sums the unit's parts with weights
-// 2^(m_i - max m).
-template <typename T>
+// A block: 32 rows (lanes) and four columns of one unit; its four warps take every fourth part of the
+// unit, with a running maximum each, and add up in shared memory with weights 2^(m_i - max m).
+// Latency bound (a few KB per block): the loads of four parts are in flight together.
+template <typename T, int ROWS, int KT>
 __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
-                                                    int ROWS_, int KT_, int hd_pad) {
-  const int rows_all = a.nodes * a.group, blocks = (rows_all + ROWS_ - 1) / ROWS_;
-  const int lane = threadIdx.x & 31;
-  const int unit = blockIdx.x, kvh = unit / blocks % a.n_kv, blk = unit % blocks;
-  const int b = unit / blocks / a.n_kv;
-  auto tiles = [&](int e) {
-    return (int64_t)(cached_rows(a, e) + KT_ - 1) / KT_ + (a.nodes + KT_ - 1) / KT_;
-  };
-  int64_t before = 0, total = 0;
-  for (int e = lane; e < a.batch; e += 32) {
-    const int64_t n = tiles(e) * a.n_kv * blocks;
-    total += n;
-    if (e < b) before += n;
-  }
+                                                    int hd_pad) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  __shared__ float part[4][6][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+  TreeLine<ROWS, KT> line;
+  line.begin(a, grid, 0);
+  const int rows_all = a.nodes * a.group, unit = blockIdx.x;
+  const int kvh = unit / line.blocks % a.n_kv, blk = unit % line.blocks;
+  const int b = unit / line.blocks / a.n_kv;
+  int64_t before = 0;
+  for (int e = lane; e < b; e += 32) before += line.entry_tiles(a, e);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    total += __shfl_xor_sync(0xffffffffu, total, o);
-    before += __shfl_xor_sync(0xffffffffu, before, o);
-  }
-  const int64_t n = tiles(b), u0 = before + ((int64_t)kvh * blocks + blk) * n, u1 = u0 + n;
-  const int c0 = share_owner(total, grid, u0), c1 = share_owner(total, grid, u1 - 1);
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  const int n = (cached_rows(a, b) + KT - 1) / KT + line.draft_tiles;
+  const int64_t u0 = before + (int64_t)(kvh * line.blocks + blk) * n;
+  const int c0 = (int)(u0 / line.per), c1 = (int)((u0 + n - 1) / line.per);
   if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
-  const int n_rows = min(ROWS_, rows_all - blk * ROWS_);
-  const int chunks = (n_rows + 31) / 32, cols = (a.head_dim + 3) / 4;
-  const size_t slot_floats = dense_slot_floats(ROWS_, hd_pad);
-  const float *ws = static_cast<const float *>(a.ws);
-  const int warp = blockIdx.y * (blockDim.x / 32) + threadIdx.x / 32;
-  if (warp >= chunks * cols) return;
-  const int r = warp / cols * 32 + lane, c4 = warp % cols;
-  const int pr = blk * ROWS_ + min(r, n_rows - 1), node = pr / a.group;
+  const int n_rows = min(ROWS, rows_all - blk * ROWS);
+  const int cols = (a.head_dim + 3) / 4, c4 = blockIdx.y % cols;
+  const int r = blockIdx.y / cols * 32 + lane;
+  if (r - lane >= n_rows) return;
+  const int pr = blk * ROWS + min(r, n_rows - 1), node = pr / a.group;
+  const size_t slot_floats = dense_slot_floats(ROWS, hd_pad);
+  // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's share:
+  // slot 0.
+  const float *ws = static_cast<const float *>(a.ws) + (min(r, n_rows - 1));
+  const int first_slot = 2 * c0 + 1;
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int c = c0 + warp; c <= c1; c += 16) {
+    float mi[4], li[4];
+    float4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      mi[i] = -INFINITY;
+      li[i] = 0.f;
+      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (c + 4 * i <= c1) {
+        const float *w = ws + (c + 4 * i == c0 ? first_slot : 2 * (c + 4 * i)) * slot_floats;
+        mi[i] = w[(size_t)ROWS * hd_pad];
+        li[i] = w[(size_t)ROWS * (hd_pad + 1)];
+        v[i] = *reinterpret_cast<const float4 *>(
+            static_cast<const float *>(a.ws) +
+            (c + 4 * i == c0 ? first_slot : 2 * (c + 4 * i)) * slot_floats +
+            ((size_t)c4 * ROWS + min(r, n_rows - 1)) * 4);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (mi[i] == -INFINITY && li[i] == 0.f) continue;  // a part that saw nothing
+      const float mn = fmaxf(m, mi[i]), ref = mn == -INFINITY ? 0.f : mn;
+      const float f = ex2(m - ref), g = ex2(mi[i] - ref);
+      m = mn;
+      l = l * f + li[i] * g;
+      o[0] = o[0] * f + v[i].x * g;
+      o[1] = o[1] * f + v[i].y * g;
+      o[2] = o[2] * f + v[i].z * g;
+      o[3] = o[3] * f + v[i].w * g;
+    }
+  }
+  part[warp][0][lane] = m;
+  part[warp][1][lane] = l;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) part[warp][2 + e][lane] = o[e];
+  __syncthreads();
+  if (warp) return;
+  float top = m;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
+  const float ref = top == -INFINITY ? 0.f : top;
+  l = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ex2(part[w][0][lane] - ref);
+    l += part[w][1][lane] * f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] += part[w][2 + e][lane] * f;
+  }
   uint32_t mask[4];
   node_mask(a, a.parents + (int64_t)b * a.nodes, node, mask);
   if (r >= n_rows) return;
-  float m = -INFINITY;
-  auto slot = [&](int c) {
-    return ws + (2 * c + (share_begin(total, grid, c) > u0 ? 0 : 1)) * slot_floats;
-  };
-  for (int c = c0; c <= c1; ++c)
-    if (share_begin(total, grid, c + 1) > share_begin(total, grid, c))
-      m = fmaxf(m, slot(c)[(size_t)ROWS_ * hd_pad + r]);
-  float l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int c = c0; c <= c1; ++c) {
-    if (share_begin(total, grid, c + 1) <= share_begin(total, grid, c)) continue;
-    const float *w = slot(c);
-    const float mi = w[(size_t)ROWS_ * hd_pad + r], li = w[(size_t)ROWS_ * (hd_pad + 1) + r];
-    if (mi == -INFINITY && !(li != li)) continue;  // a part that saw nothing
-    const float f = exp2f(mi - m);
-    const float4 v = reinterpret_cast<const float4 *>(w)[(size_t)c4 * ROWS_ + r];
-    l = fmaf(li, f, l);
-    o[0] = fmaf(v.x, f, o[0]);
-    o[1] = fmaf(v.y, f, o[1]);
-    o[2] = fmaf(v.z, f, o[2]);
-    o[3] = fmaf(v.w, f, o[3]);
-  }
   const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) && l != 0.f;
+  const float inv = 1.f / l;
   T *out = static_cast<T *>(a.out.data) +
            at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (c4 * 4 + e < a.head_dim) out[c4 * 4 + e] = from_f<T>(live ? o[e] / l : 0.f);
+    if (c4 * 4 + e < a.head_dim) out[c4 * 4 + e] = from_f<T>(live ? o[e] * inv : 0.f);
 }
 
 template <typename T, int HD, bool TREE, bool VEC>
@@ -385,15 +405,29 @@ cudaError_t run(const DenseArgs &a, int grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, cudaStream_t s) {
-  const int blocks = (a.nodes * a.group + rows - 1) / rows;
-  const int warps = ((rows < a.nodes * a.group ? rows : a.nodes * a.group) + 31) / 32 *
-                    ((a.head_dim + 3) / 4);
-  const dim3 g((unsigned)(a.batch * a.n_kv * blocks), (unsigned)((warps + 3) / 4));
+  const int all = a.nodes * a.group, blocks = (all + rows - 1) / rows;
+  const int chunks = ((rows < all ? rows : all) + 31) / 32;
+  cudaLaunchAttribute attr = {};
+  // The launch overlaps the end of the kernel before it; the kernel itself waits for its results.
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.batch * a.n_kv * blocks),
+                     (unsigned)(chunks * ((a.head_dim + 3) / 4)));
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const int pad = dense_hd_pad(a.head_dim);
+  cudaError_t e = cudaErrorInvalidValue;
   with_dtype(a.dtype, [&](auto tag) {
-    k_dense_join<decltype(tag)><<<g, 128, 0, s>>>(a, grid, rows, keys, dense_hd_pad(a.head_dim));
+    using T = decltype(tag);
+    if (keys == 64) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64>, a, grid, pad);
+    else if (rows == 128) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128>, a, grid, pad);
+    else e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128>, a, grid, pad);
   });
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_dense_cc(const DenseArgs &a, cudaStream_t s) {

@@ -45,6 +45,7 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;  // log2 of the growth of a row's maximum that is left in P
 enum { MODE_PROMPT = 0, MODE_ROWS = 1, MODE_KEYS = 2 };
 constexpr int MAX_SLOTS = 8;
+constexpr int POLY = 6;  // of 16 exponentials, how many take the FMA pipe
 
 struct Maps {
   CUtensorMap k, v, kc, vc;  // kc, vc: tree
@@ -58,7 +59,7 @@ struct Ctl {
   // says nothing about it), the check has passed it. A phase each per checked use of the slot, which
   // is not refilled before the MMA has read it.
   uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];  // p_full: per half of the keys
   uint64_t both, drain;
   uint32_t tmem;
   int abort;
@@ -102,16 +103,6 @@ ISKV_DEV void tmem_ld32(uint32_t taddr, float *v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-ISKV_DEV void tmem_st32(uint32_t taddr, const float *v) {
-  uint32_t r[16];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[16 * h + i]);
-    tmem_st16(taddr + 16 * h, r);
-  }
-}
-
 ISKV_DEV float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -136,6 +127,52 @@ ISKV_DEV float2 add2(float2 a, float2 b) {
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
+}
+
+ISKV_DEV float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+ISKV_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+ISKV_DEV float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^x for two values on the FMA pipe (the exponential unit's 16 a clock are not enough for both
+// streams). x = n + f, n the nearest integer: adding 1.5 2^23 + 127 leaves n + 127 in the low bits,
+// which shifted by 23 are the float 2^n (0 for n = -127); 2^f is a polynomial with p(0) = 1, fitted
+// for the smallest largest relative error on [-1/2, 1/2]: degree 3, 1.0e-4, for bf16 (half a step
+// of P is 3.9e-3), degree 4, 2.8e-6, for fp16 (4.9e-4). x <= 14; -inf gives 0, NaN stays NaN.
+template <typename T>
+ISKV_DEV float2 poly_ex2(float2 x) {
+  constexpr float MAGIC = 12582912.f + 127.f;
+  x.x = max_nan(x.x, -127.f);
+  x.y = max_nan(x.y, -127.f);
+  const float2 r = add2(x, make_float2(MAGIC, MAGIC));
+  const float2 f = add2(x, fma2(r, make_float2(-1.f, -1.f), make_float2(MAGIC, MAGIC)));
+  float2 p;
+  if constexpr (std::is_same<T, __half>::value) {
+    p = fma2(make_float2(0.009582853f, 0.009582853f), f, make_float2(0.055906426f, 0.055906426f));
+    p = fma2(p, f, make_float2(0.24024099f, 0.24024099f));
+    p = fma2(p, f, make_float2(0.69312418f, 0.69312418f));
+  } else {
+    p = fma2(make_float2(0.055008933f, 0.055008933f), f, make_float2(0.24221095f, 0.24221095f));
+    p = fma2(p, f, make_float2(0.6932829f, 0.6932829f));
+  }
+  p = fma2(p, f, make_float2(1.f, 1.f));
+  return mul2(p, make_float2(__int_as_float(__float_as_int(r.x) << 23),
+                             __int_as_float(__float_as_int(r.y) << 23)));
 }
 
 template <typename T>
@@ -173,37 +210,25 @@ ISKV_DEV int64_t at(const iskv_heads &x, int64_t b, int64_t row, int64_t head) {
 // The CTA's units in order, the same for every warp (whole-warp calls).
 template <int MODE, int ROWS>
 struct Walk {
-  int64_t x = 0, end = 0;
+  TreeLine<ROWS, KT> line;
   int count = 0;  // units handed out so far
 
   ISKV_DEV void begin(const DenseArgs &a) {
-    if constexpr (MODE != MODE_PROMPT) {
-      const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
-      const int64_t total = total_tiles<KT>(a, blocks);
-      x = share_begin(total, gridDim.x, blockIdx.x);
-      end = share_begin(total, gridDim.x, blockIdx.x + 1);
-    }
+    if constexpr (MODE != MODE_PROMPT) line.begin(a, gridDim.x, blockIdx.x);
   }
   ISKV_DEV bool next(const DenseArgs &a, Unit &u) {
     if constexpr (MODE == MODE_PROMPT) {
-      if (count++) return false;
-      if (!find_prompt_unit<ROWS>(a, blockIdx.x / a.n_kv, u)) return false;
-      u.kvh = blockIdx.x % a.n_kv;
+      const int rank = blockIdx.x / a.n_kv;
+      if (count || !find_prompt_unit<ROWS>(a, rank, u)) return false;
+      u.kvh = blockIdx.x - rank * a.n_kv;
       u.t0 = 0;
       u.t1 = u.n_tiles = last_token(a, u) / KT + 1;
       u.cache_tiles = 0;
-      return true;
     } else {
-      if (x >= end) return false;
-      const int blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
-      int64_t start;
-      const int b = find_entry<KT>(a, blocks, x, start);
-      if (b < 0) return false;
-      tree_unit<ROWS, KT>(a, b, start, x, end, u);
-      x += u.t1 - u.t0;
-      ++count;
-      return true;
+      if (!line.next(a, u)) return false;
     }
+    ++count;
+    return true;
   }
 };
 
@@ -237,6 +262,7 @@ __global__ void __launch_bounds__(384, 1)
     k_dense_tc(const __grid_constant__ DenseArgs a, const __grid_constant__ Maps maps) {
   using C = Cfg<HD, MODE>;
   constexpr bool TREE = MODE != MODE_PROMPT;
+  if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ char raw[];
   char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
   Ctl &ctl = *reinterpret_cast<Ctl *>(base + (C::NQ + C::SLOTS) * C::TILE);
@@ -254,7 +280,8 @@ __global__ void __launch_bounds__(384, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.q_full[i], MODE == MODE_KEYS ? 8 : 4);
       mbar_init(&ctl.s_full[i], 1);
-      mbar_init(&ctl.p_full[i], 4);
+      mbar_init(&ctl.p_full[i][0], 4);
+      mbar_init(&ctl.p_full[i][1], 4);
       mbar_init(&ctl.o_full[i], 1);
     }
     mbar_init(&ctl.both, 8);
@@ -310,28 +337,31 @@ __global__ void __launch_bounds__(384, 1)
       // Queries into shared memory: K-major, 128-byte swizzle; the scale's sign goes with them. (A
       // stream without tiles skips the unit, so that it cannot run ahead of the MMA warp.)
       if (MODE == MODE_KEYS || n_mine > 0) {
-        constexpr int CH = HD / 8;
+        // Every warp its own 32 rows (in MODE_KEYS half of their columns), all loads in flight at
+        // once; lane i holds row i's address.
+        constexpr int CH = HD / 8, CW = MODE == MODE_KEYS ? CH / 2 : CH, N = CW;
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-        const T *q = static_cast<const T *>(a.q.data);
-        // Every warp its own 32 rows (in MODE_KEYS half of their columns).
-        constexpr int CW = MODE == MODE_KEYS ? CH / 2 : CH;
-#pragma unroll 8
-        for (int i = lane; i < 32 * CW; i += 32) {
-          const int r = (warp & 3) * 32 + i / CW;
-          const int ch = i % CW + (MODE == MODE_KEYS ? st * CW : 0);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (r < tile_rows && ch * 8 < a.head_dim) {
-            const int pr = u.row0 + row_off + r;
-            x = *reinterpret_cast<const uint4 *>(
-                q + at(a.q, entry, row_base + pr / a.group,
-                       (int64_t)u.kvh * a.group + pr % a.group) + ch * 8);
-            x.x ^= flip;
-            x.y ^= flip;
-            x.z ^= flip;
-            x.w ^= flip;
-          }
+        const int w0 = (warp & 3) * 32, pr = u.row0 + row_off + w0 + lane, tk = pr / a.group;
+        const uint64_t row_at = reinterpret_cast<uint64_t>(
+            static_cast<const T *>(a.q.data) +
+            at(a.q, entry, row_base + tk, (int64_t)u.kvh * a.group + (pr - tk * a.group)));
+        uint4 x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = (32 * i + lane) / CW;
+          const int ch = lane % CW + (MODE == MODE_KEYS ? st * CW : 0);
+          const uint64_t src = __shfl_sync(0xffffffffu, row_at, r);
+          x[i] = make_uint4(0, 0, 0, 0);
+          if (w0 + r < tile_rows && ch * 8 < a.head_dim)
+            x[i] = *reinterpret_cast<const uint4 *>(src + ch * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int r = w0 + (32 * i + lane) / CW;
+          const int ch = lane % CW + (MODE == MODE_KEYS ? st * CW : 0);
           *reinterpret_cast<uint4 *>(q_tile + (ch / 8) * 16384 + r * 128 +
-                                     (((ch & 7) ^ (r & 7)) * 16)) = x;
+                                     (((ch & 7) ^ (r & 7)) * 16)) =
+              make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -354,8 +384,10 @@ __global__ void __launch_bounds__(384, 1)
         fence_after_sync();
         if (busy) {
           float s[128];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
+          tmem_ld32(s_tm, s);
+          tmem_ld32(s_tm + 32, s + 32);
+          tmem_ld32(s_tm + 64, s + 64);
+          tmem_ld32(s_tm + 96, s + 96);
           tmem_ld_wait();
           int r0, r1;
           if (hidden_rows<MODE>(a, u, t, r0, r1)) {
@@ -371,10 +403,12 @@ __global__ void __launch_bounds__(384, 1)
           }
           float top[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) top[j] = s[j];
+          for (int j = 0; j < 4; ++j) top[j] = fmaxf(s[j], s[j + 4]);
 #pragma unroll
-          for (int j = 4; j < 128; ++j) top[j & 3] = fmaxf(top[j & 3], s[j]);
-          const float mn = fmaxf(m, fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])));
+          for (int j = 8; j < 128; j += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[j + e], s[j + e + 4]);
+          const float mn = max3(max3(m, top[0], top[1]), top[2], top[3]);
           const bool grow = mn > m && (m == -INFINITY || (mn - m) * c > LAZY);
           if (__any_sync(0xffffffffu, grow)) {
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
@@ -382,14 +416,15 @@ __global__ void __launch_bounds__(384, 1)
             m = mn;
             // S(i) complete: so is the previous P V of this stream, which was issued before it
             if (i > 0) {
-#pragma unroll
-              for (int j = 0; j < HD / 32; ++j) {
-                float o[32];
-                tmem_ld32(o_tm + 32 * j, o);
+#pragma unroll 1
+              for (int j = 0; j < HD / 16; ++j) {
+                float o[16];
+                tmem_ld16(o_tm + 16 * j, o);
                 tmem_ld_wait();
+                uint32_t r[16];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) o[e] *= f;
-                tmem_st32(o_tm + 32 * j, o);
+                for (int e = 0; e < 16; ++e) r[e] = __float_as_uint(o[e] * f);
+                tmem_st16(o_tm + 16 * j, r);
               }
             }
           }
@@ -402,19 +437,32 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float2 x = fma2(make_float2(s[32 * j + 2 * e], s[32 * j + 2 * e + 1]), c2, off2);
-              x.x = ex2(x.x);
-              x.y = ex2(x.y);
+              if (e * POLY % 16 < POLY) {
+                x = poly_ex2<T>(x);
+              } else {
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+              }
               sum[e & 1] = add2(sum[e & 1], x);
               p[e] = pack2<T>(x.x, x.y);
             }
             tmem_st16(s_tm + 16 * j, p);
+            if (j == 1) {  // the second product starts on the first half
+              tmem_st_wait();
+              fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&ctl.p_full[st][0]);
+            }
           }
           l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
           tmem_st_wait();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ctl.p_full[st][1]);
+        } else if (lane == 0) {
+          mbar_arrive(&ctl.p_full[st][0]);
+          mbar_arrive(&ctl.p_full[st][1]);
         }
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl.p_full[st]);
       }
       if (!ok) break;
 
@@ -515,15 +563,14 @@ __global__ void __launch_bounds__(384, 1)
                    at(a.out, entry, row_base + pr / a.group,
                       (int64_t)u.kvh * a.group + pr % a.group);
           const int n_rows = min(32, tile_rows - (warp & 3) * 32);
-          const int ch0 = c0 / 8, chn = (c1 - c0) / 8;
-#pragma unroll 4
-          for (int i = lane; i < 32 * chn; i += 32) {
-            const int r = i / chn, ch = ch0 + i % chn;
-            T *dst = reinterpret_cast<T *>(
-                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(out), r));
-            const int rr = (warp & 3) * 32 + r;
+          constexpr int CN = HD / 8 / (MODE == MODE_KEYS ? 2 : 1);
+          const int ch = lane % CN + c0 / 8;
+#pragma unroll
+          for (int i = 0; i < CN; ++i) {
+            const int r = (32 * i + lane) / CN, rr = (warp & 3) * 32 + r;
+            const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), r);
             if (r < n_rows && ch * 8 < a.head_dim)
-              *reinterpret_cast<uint4 *>(dst + ch * 8) = *reinterpret_cast<const uint4 *>(
+              *reinterpret_cast<uint4 *>(dst + ch * 16) = *reinterpret_cast<const uint4 *>(
                   q_tile + (size_t)rr * HD * 2 + ((ch ^ (rr & 7)) * 16));
           }
         }
@@ -614,12 +661,14 @@ __global__ void __launch_bounds__(384, 1)
       }
       mma_commit(&ctl.s_full[s]);
     };
-    auto values = [&](int s, uint32_t v_tile, bool first) {
-      const uint64_t vd = sw128_mn_desc(v_tile, 16384);
+    // P V over the keys of one half.
+    auto values = [&](int s, int half, uint32_t v_tile, bool first) {
+      const uint64_t vd = desc_add(sw128_mn_desc(v_tile, 16384), half * 8192);
+      const uint32_t p = tmem + 128 * s + 32 * half;
 #pragma unroll
-      for (int k = 0; k < KT / 16; ++k)
-        mma_bf16_ts(tmem + O_COL + HD * s, tmem + 128 * s + 8 * k, desc_add(vd, k * 2048), ID_O,
-                    !first || k > 0);
+      for (int k = 0; k < KT / 32; ++k)
+        mma_bf16_ts(tmem + O_COL + HD * s, p + 8 * k, desc_add(vd, k * 2048), ID_O,
+                    !first || half > 0 || k > 0);
     };
     while (ok && walk.next(a, u)) {
       if (lane == 0) {
@@ -655,10 +704,13 @@ __global__ void __launch_bounds__(384, 1)
           for (int s = 0; s < 2; ++s) {
             const int mine = MODE == MODE_KEYS ? i / 2 : i;  // the stream's tile number
             if (MODE == MODE_KEYS ? (i & 1) != s : i >= n_s[s]) continue;
-            if (!wait(&ctl.p_full[s], ph_p[s])) break;
+            if (!wait(&ctl.p_full[s][0], ph_p[s])) break;
+            fence_after_sync();
+            values(s, 0, tile_at(vp), mine == 0);
+            if (!wait(&ctl.p_full[s][1], ph_p[s])) break;
             ph_p[s] ^= 1;
             fence_after_sync();
-            values(s, tile_at(vp), mine == 0);
+            values(s, 1, tile_at(vp), mine == 0);
             if (mine == n_s[s] - 1) mma_commit(&ctl.o_full[s]);
             if (MODE == MODE_KEYS) mma_commit(&ctl.kv_empty[vp.slot]);
             if (mine + 1 < n_s[s]) {
