@@ -367,7 +367,8 @@ iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, cons
  *                   records ISKV_ERR_SHAPE), or NULL: all n_cap rows. It is read on the device, so a
  *                   captured call follows the cache as it grows.
  * status, scale, head counts, types as iskv_prompt_attention. 0 <= batch <= 4096, 0 <= n_nodes <=
- * 128, 0 <= n_cap < 2^31. out must not overlap the inputs.
+ * 128, 0 <= n_cap < 2^31, and batch * n_kv_heads * ceil(n_nodes * group / 64) * (n_cap / 64 + 3) <
+ * 2^31 with group = n_q_heads / n_kv_heads. out must not overlap the inputs.
  * ws                iskv_tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads, head_dim)
  *                   bytes, 256-byte aligned (partial results of units cut between CTAs); calls that
  *                   may overlap on the device need one each.

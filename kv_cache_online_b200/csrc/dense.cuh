@@ -36,6 +36,7 @@ struct Unit {
   int cache_tiles;  // tree: key tiles over the cache (the drafted nodes' follow)
   int n_tiles;
   int t0, t1;
+  int open;       // first key row that not every row of the unit sees (prompt: token; tree: cached row)
 };
 
 // Rows [lo, hi) of sequence s; an inconsistent entry counts as empty and is reported.
@@ -127,44 +128,42 @@ ISKV_DEV int cached_rows(const DenseArgs &a, int b) {
   return n;
 }
 
-// The line of a tree call's tiles and a CTA's way along its share of it (whole-warp calls). Shares are
-// `per` tiles each, the last ones may be empty.
+// The line of a tree call's tiles (fewer than 2^31, which the entry point checks) and a CTA's way along
+// its share of it (whole-warp calls). Shares are `per` tiles each, the last ones may be empty.
 template <int ROWS, int KT>
 struct TreeLine {
   int blocks, draft_tiles;
-  int len0;         // cached rows of entry `lane`: the first 32 entries stay in registers
-  int64_t total, per, x, end;
+  int len0;  // cached rows of entry `lane`: the first 32 entries stay in registers
+  int per, x, end;
 
-  ISKV_DEV int len_of(const DenseArgs &a, int b) const {  // lane-varying b
-    return b < 32 ? len0 : cached_rows(a, b);
-  }
-  ISKV_DEV int64_t entry_tiles(const DenseArgs &a, int b) const {
-    return b < a.batch ? (int64_t)((len_of(a, b) + KT - 1) / KT + draft_tiles) * (a.n_kv * blocks) : 0;
+  // b: the lane itself or from 32 on
+  ISKV_DEV int len_of(const DenseArgs &a, int b) const { return b < 32 ? len0 : cached_rows(a, b); }
+  ISKV_DEV int entry_tiles(const DenseArgs &a, int b) const {
+    return b < a.batch ? ((len_of(a, b) + KT - 1) / KT + draft_tiles) * (a.n_kv * blocks) : 0;
   }
   ISKV_DEV void begin(const DenseArgs &a, int grid, int cta) {
     const int lane = threadIdx.x & 31;
     blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
     draft_tiles = (a.nodes + KT - 1) / KT;
     len0 = lane < a.batch ? cached_rows(a, lane) : 0;
-    total = 0;
+    int total = 0;
     for (int b = lane; b < a.batch; b += 32) total += entry_tiles(a, b);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-    per = (total + grid - 1) / grid;
-    x = min(total, per * cta);
-    end = min(total, x + per);
+    total = __reduce_add_sync(0xffffffffu, total);
+    per = (int)((unsigned)(total - 1) / (unsigned)grid) + 1;
+    x = (int)min((int64_t)total, (int64_t)per * cta);
+    end = min(total - x, per) + x;
   }
   // The next unit of the share, or false.
   ISKV_DEV bool next(const DenseArgs &a, Unit &u) {
     if (x >= end) return false;
     const int lane = threadIdx.x & 31;
-    int64_t before = 0;
+    int before = 0;
     for (int b0 = 0;; b0 += 32) {
-      const int64_t n = entry_tiles(a, b0 + lane);
-      int64_t sum = n;
+      const int n = entry_tiles(a, b0 + lane);
+      int sum = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xffffffffu, sum, o);
+        const int t = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o) sum += t;
       }
       const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
@@ -172,7 +171,7 @@ struct TreeLine {
         const int l = __ffs(past) - 1;
         before += __shfl_sync(0xffffffffu, sum - n, l);
         u.b = b0 + l;
-        u.len = __shfl_sync(0xffffffffu, len_of(a, b0 + lane), l);
+        u.len = __shfl_sync(0xffffffffu, b0 + lane < a.batch ? len_of(a, b0 + lane) : 0, l);
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -181,13 +180,12 @@ struct TreeLine {
     u.cache_tiles = (u.len + KT - 1) / KT;
     u.n_tiles = u.cache_tiles + draft_tiles;
     const int all_rows = a.nodes * a.group;
-    const int64_t off = x - before;
-    const int idx = off >> 31 ? (int)(off / u.n_tiles) : (int)off / u.n_tiles;
-    u.kvh = idx / blocks;
+    const int idx = (x - before) / u.n_tiles;
+    u.kvh = blocks == 1 ? idx : idx / blocks;
     u.row0 = (idx - u.kvh * blocks) * ROWS;
     u.n_rows = min(ROWS, all_rows - u.row0);
-    u.t0 = (int)(off - (int64_t)idx * u.n_tiles);
-    u.t1 = (int)min((int64_t)u.n_tiles, u.t0 + (end - x));
+    u.t0 = x - before - idx * u.n_tiles;
+    u.t1 = min(u.n_tiles, u.t0 + (end - x));
     x += u.t1 - u.t0;
     return true;
   }

@@ -192,6 +192,11 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   if (st == ISKV_OK) st = check_status_word(status, who);
   if (st != ISKV_OK) return st;
   if (empty) return ISKV_OK;
+  // The line of key tiles is counted in 32 bits; no kernel's tiles or row blocks are smaller than 64.
+  const int64_t blocks = (n_nodes * (n_q_heads / n_kv_heads) + 63) / 64;
+  if ((int64_t)batch * n_kv_heads * blocks >= ((int64_t)1 << 31) / (n_cap / 64 + 3))
+    return fail(ISKV_ERR_SHAPE, "%s: batch * n_kv_heads * row blocks * key tiles must stay below "
+                "2^31", who);
   if (!parents || reinterpret_cast<uintptr_t>(parents) % 4 ||
       reinterpret_cast<uintptr_t>(n_cached) % 4)
     return fail(ISKV_ERR_ARG, "%s: null or misaligned parents / n_cached", who);

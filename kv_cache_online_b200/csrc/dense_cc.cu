@@ -246,13 +246,15 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
     for (int i = 0; i < 4; ++i) {
       const int r = ty * 4 + i;
       if (r >= u.n_rows) continue;
+      const bool live =
+          sm.mask[tok[i]][0] | sm.mask[tok[i]][1] | sm.mask[tok[i]][2] | sm.mask[tok[i]][3];
 #pragma unroll
       for (int n = 0; n < NC; ++n)
         reinterpret_cast<float4 *>(ws)[(tx + 16 * n) * ROWS + r] =
             make_float4(o[i][n][0], o[i][n][1], o[i][n][2], o[i][n][3]);
       if (tx == 0) {
-        ws[ROWS * HD + r] = m[i];
-        ws[ROWS * (HD + 1) + r] = l[i];
+        ws[ROWS * HD + r] = live ? m[i] : -INFINITY;
+        ws[ROWS * (HD + 1) + r] = live ? l[i] : 0.f;
       }
     }
   }
@@ -309,13 +311,12 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int rows_all = a.nodes * a.group, unit = blockIdx.x;
   const int kvh = unit / line.blocks % a.n_kv, blk = unit % line.blocks;
   const int b = unit / line.blocks / a.n_kv;
-  int64_t before = 0;
+  int before = 0;
   for (int e = lane; e < b; e += 32) before += line.entry_tiles(a, e);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  before = __reduce_add_sync(0xffffffffu, before);
   const int n = (cached_rows(a, b) + KT - 1) / KT + line.draft_tiles;
-  const int64_t u0 = before + (int64_t)(kvh * line.blocks + blk) * n;
-  const int c0 = (int)(u0 / line.per), c1 = (int)((u0 + n - 1) / line.per);
+  const int u0 = before + (kvh * line.blocks + blk) * n;
+  const int c0 = u0 / line.per, c1 = (u0 + n - 1) / line.per;
   if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
   const int n_rows = min(ROWS, rows_all - blk * ROWS);
   const int cols = (a.head_dim + 3) / 4, c4 = blockIdx.y % cols;
@@ -379,10 +380,8 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] += part[w][2 + e][lane] * f;
   }
-  uint32_t mask[4];
-  node_mask(a, a.parents + (int64_t)b * a.nodes, node, mask);
   if (r >= n_rows) return;
-  const bool live = (mask[0] | mask[1] | mask[2] | mask[3]) && l != 0.f;
+  const bool live = l != 0.f;  // padding nodes came as parts that saw nothing
   const float inv = 1.f / l;
   T *out = static_cast<T *>(a.out.data) +
            at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);

@@ -20,11 +20,12 @@
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row; P goes back to tensor memory in S's
 // place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring;
-// 9 issues the MMAs; 10-11 look through value tiles of which some row must not see some key, and
-// replace what is not finite by zero before the MMA reads it (0 * NaN would reach every row); if
-// such a value is seen by some row, the epilogue adds it to exactly the rows that see it.
+// 9 issues the MMAs; 10-11 look through value tiles of which some row must not see some key, and replace what is not finite by zero before the MMA
+// reads it (0 * NaN would reach every row); if such a value is seen by some row, the epilogue adds
+// it to exactly the rows that see it.
 //
-// Tensor memory (512 columns): S0, S1 at 0 and 128 (P over their first 64), O0, O1 at 256.
+// Tensor memory (512 columns): two S of 128 x 64 per stream at 0 and 128 (P over the first half of
+// each), O0, O1 at 256.
 #include "dense.cuh"
 #include "profiling.h"
 #include "tc_sm100.cuh"
@@ -45,7 +46,7 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;  // log2 of the growth of a row's maximum that is left in P
 enum { MODE_PROMPT = 0, MODE_ROWS = 1, MODE_KEYS = 2 };
 constexpr int MAX_SLOTS = 8;
-constexpr int POLY = 6;  // of 16 exponentials, how many take the FMA pipe
+constexpr int POLY = 0;  // of 16 exponentials, how many take the FMA pipe
 
 struct Maps {
   CUtensorMap k, v, kc, vc;  // kc, vc: tree
@@ -59,7 +60,7 @@ struct Ctl {
   // says nothing about it), the check has passed it. A phase each per checked use of the slot, which
   // is not refilled before the MMA has read it.
   uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
-  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2];  // p_full: per half of the keys
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2];  // [stream][half of the tile's keys]
   uint64_t both, drain;
   uint32_t tmem;
   int abort;
@@ -74,9 +75,10 @@ struct Cfg {
   static constexpr int ROWS = 128 * NQ;                     // packed rows of a unit
   static constexpr int AHEAD = MODE == MODE_KEYS ? 2 : 1;   // key tiles ahead of the value tile
   // As many ring slots as fit beside the query tiles in 227 KB, at most 8.
-  static constexpr int FIT = (232448 - 1024 - (int)sizeof(Ctl) - NQ * TILE) / TILE;
+  static constexpr int REST = (int)sizeof(Ctl) + (MODE == MODE_KEYS ? 2048 : 0);  // + m, l of the streams
+  static constexpr int FIT = (232448 - REST - NQ * TILE) / TILE;
   static constexpr int SLOTS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
-  static constexpr int SMEM = 1024 + NQ * TILE + SLOTS * TILE + (int)sizeof(Ctl);
+  static constexpr int SMEM = NQ * TILE + SLOTS * TILE + REST;
 };
 
 ISKV_DEV void tma_load_4d(uint32_t dst, const CUtensorMap *map, int x, int y, int z, int w,
@@ -109,35 +111,6 @@ ISKV_DEV float ex2(float x) {
   return y;
 }
 
-// Two float32 at once (the packed FMA and add of sm_100).
-ISKV_DEV float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-  return d;
-}
-ISKV_DEV float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
-
-ISKV_DEV float2 mul2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\t"
-      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-  return d;
-}
 ISKV_DEV float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -149,32 +122,6 @@ ISKV_DEV float max_nan(float a, float b) {
   return d;
 }
 
-// 2^x for two values on the FMA pipe (the exponential unit's 16 a clock are not enough for both
-// streams). x = n + f, n the nearest integer: adding 1.5 2^23 + 127 leaves n + 127 in the low bits,
-// which shifted by 23 are the float 2^n (0 for n = -127); 2^f is a polynomial with p(0) = 1, fitted
-// for the smallest largest relative error on [-1/2, 1/2]: degree 3, 1.0e-4, for bf16 (half a step
-// of P is 3.9e-3), degree 4, 2.8e-6, for fp16 (4.9e-4). x <= 14; -inf gives 0, NaN stays NaN.
-template <typename T>
-ISKV_DEV float2 poly_ex2(float2 x) {
-  constexpr float MAGIC = 12582912.f + 127.f;
-  x.x = max_nan(x.x, -127.f);
-  x.y = max_nan(x.y, -127.f);
-  const float2 r = add2(x, make_float2(MAGIC, MAGIC));
-  const float2 f = add2(x, fma2(r, make_float2(-1.f, -1.f), make_float2(MAGIC, MAGIC)));
-  float2 p;
-  if constexpr (std::is_same<T, __half>::value) {
-    p = fma2(make_float2(0.009582853f, 0.009582853f), f, make_float2(0.055906426f, 0.055906426f));
-    p = fma2(p, f, make_float2(0.24024099f, 0.24024099f));
-    p = fma2(p, f, make_float2(0.69312418f, 0.69312418f));
-  } else {
-    p = fma2(make_float2(0.055008933f, 0.055008933f), f, make_float2(0.24221095f, 0.24221095f));
-    p = fma2(p, f, make_float2(0.6932829f, 0.6932829f));
-  }
-  p = fma2(p, f, make_float2(1.f, 1.f));
-  return mul2(p, make_float2(__int_as_float(__float_as_int(r.x) << 23),
-                             __int_as_float(__float_as_int(r.y) << 23)));
-}
-
 template <typename T>
 ISKV_DEV uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -182,6 +129,62 @@ ISKV_DEV uint32_t pack2(float a, float b) {
     return *reinterpret_cast<uint32_t *>(&h);
   } else {
     return pack_bf16(a, b);
+  }
+}
+
+// The weights 2^(s c + off) of 32 scores, in place, as 16 packed pairs, and their sum. POLY of the 16
+// pairs take the FMA pipe (the exponential unit's 16 a clock are not enough for both streams):
+// x = n + f, n the nearest integer: adding 1.5 2^23 + 127 leaves n + 127 in the low bits, which
+// shifted by 23 are the float 2^n (0 for n = -127); 2^f is a polynomial with p(0) = 1, fitted for
+// the smallest largest relative error on [-1/2, 1/2]: degree 3, 1.0e-4, for bf16 (half a step of P
+// is 3.9e-3), degree 4, 2.8e-6, for fp16 (4.9e-4). x <= 14; -inf gives 0, NaN stays NaN.
+// Step by step over all pairs, so that no instruction waits for the one before it.
+template <typename T>
+ISKV_DEV void weights(float *s, float c, float off, float2 (&sum)[2], uint32_t (&p)[16]) {
+  constexpr float MAGIC = 12582912.f + 127.f;
+  constexpr bool H = std::is_same<T, __half>::value;
+  auto both = [](float v) { return make_float2(v, v); };
+  auto poly = [](int e) { return e * POLY % 16 < POLY; };
+  float2 x[16], r[16], q[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) x[e] = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), both(c), both(off));
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e)) {
+      x[e] = make_float2(max_nan(x[e].x, -127.f), max_nan(x[e].y, -127.f));
+      r[e] = __fadd2_rn(x[e], both(MAGIC));
+    } else {
+      x[e].x = ex2(x[e].x);
+      x[e].y = ex2(x[e].y);
+    }
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e)) x[e] = __fadd2_rn(x[e], __ffma2_rn(r[e], both(-1.f), both(MAGIC)));
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e))
+      q[e] = H ? __ffma2_rn(both(0.009582853f), x[e], both(0.055906426f))
+               : __ffma2_rn(both(0.055008933f), x[e], both(0.24221095f));
+  if constexpr (H) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e)
+      if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(0.24024099f));
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(H ? 0.69312418f : 0.6932829f));
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(1.f));
+#pragma unroll
+  for (int e = 0; e < 16; ++e)
+    if (poly(e))
+      x[e] = __fmul2_rn(q[e], make_float2(__int_as_float(__float_as_int(r[e].x) << 23),
+                                    __int_as_float(__float_as_int(r[e].y) << 23)));
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    sum[e & 1] = __fadd2_rn(sum[e & 1], x[e]);
+    p[e] = pack2<T>(x[e].x, x[e].y);
   }
 }
 
@@ -224,37 +227,69 @@ struct Walk {
       u.t0 = 0;
       u.t1 = u.n_tiles = last_token(a, u) / KT + 1;
       u.cache_tiles = 0;
+      u.open = first_token(a, u) + 1;
     } else {
       if (!line.next(a, u)) return false;
+      u.open = u.len;
     }
     ++count;
     return true;
   }
 };
 
-// Tiles that stream s takes of the unit.
+// Half tiles (64 keys) that stream s takes of the unit.
 template <int MODE>
-ISKV_DEV int stream_tiles(const DenseArgs &a, const Unit &u, int s) {
-  const int n = u.t1 - u.t0;
-  if (MODE == MODE_KEYS) return (n + 1 - s) / 2;
-  if (u.n_rows <= 128 * s) return 0;
-  if (MODE == MODE_ROWS) return n;
-  return (u.row0 + min(u.n_rows, 128 * (s + 1)) - 1) / a.group / KT + 1;
+ISKV_DEV int stream_halves(const DenseArgs &a, const Unit &u, int s) {
+  if (MODE == MODE_PROMPT)
+    return u.n_rows <= 128 * s
+               ? 0
+               : (u.row0 + min(u.n_rows, 128 * (s + 1)) - 1) / a.group / (KT / 2) + 1;
+  const int n = u.t1 - u.t0, tiles = MODE == MODE_KEYS ? (n + 1 - s) / 2 : u.n_rows > 128 * s ? n : 0;
+  if (tiles == 0) return 0;
+  // The stream's last tile may have nothing in its second half.
+  const int t = MODE == MODE_KEYS ? u.t0 + 2 * tiles - 2 + s : u.t1 - 1;
+  const int keys = t < u.cache_tiles ? u.len - t * KT : a.nodes - (t - u.cache_tiles) * KT;
+  return 2 * tiles - (keys <= KT / 2);
 }
 
-// Rows [r0, r1) of value tile t that some row of the unit must not see; false: none.
+// First key row of tile t that some row of the unit must not see (>= KT: all rows see all keys).
 template <int MODE>
-ISKV_DEV bool hidden_rows(const DenseArgs &a, const Unit &u, int t, int &r0, int &r1) {
-  r1 = KT;
-  if (MODE == MODE_PROMPT) {
-    r0 = max(0, first_token(a, u) + 1 - t * KT);
-  } else if (t < u.cache_tiles) {
-    r0 = u.len - t * KT;
-  } else {
-    r0 = 0;
-    r1 = a.nodes;
-  }
-  return r0 < r1;
+ISKV_DEV int hidden_from(const Unit &u, int t) {
+  return MODE == MODE_PROMPT || t < u.cache_tiles ? u.open - t * KT : 0;
+}
+
+// One lane of the warp (all lanes ask): 1 for it, 0 for the others.
+ISKV_DEV uint32_t elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
+}
+// The tcgen05 instructions issued by the lane with `leader` set.
+ISKV_DEV void mma_ss(uint32_t leader, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                     uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate ? 1u : 0u), "r"(leader)
+      : "memory");
+}
+ISKV_DEV void mma_ts(uint32_t leader, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                     uint32_t id, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %5, 0;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate ? 1u : 0u), "r"(leader)
+      : "memory");
+}
+ISKV_DEV void commit(uint32_t leader, uint64_t *bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(
+          smem_u32(bar)),
+      "r"(leader)
+      : "memory");
 }
 
 template <typename T, int HD, int MODE>
@@ -263,13 +298,18 @@ __global__ void __launch_bounds__(384, 1)
   using C = Cfg<HD, MODE>;
   constexpr bool TREE = MODE != MODE_PROMPT;
   if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
-  extern __shared__ char raw[];
-  char *base = reinterpret_cast<char *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  extern __shared__ __align__(1024) char base[];
   Ctl &ctl = *reinterpret_cast<Ctl *>(base + (C::NQ + C::SLOTS) * C::TILE);
   const uint32_t q_smem = smem_u32(base), ring_smem = q_smem + C::NQ * C::TILE;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  // (a shuffle, so that the compiler knows it uniform)
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x / 32, 0), lane = threadIdx.x & 31;
   volatile int *abort = &ctl.abort;
 
+  // The swizzle needs tiles on 1,024 bytes, which the declaration asks for.
+  if (q_smem & 1023) {
+    if (threadIdx.x == 0) report(a.status, ISKV_ERR_ARG);
+    return;
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&ctl.kv_full[i], 1);
@@ -279,7 +319,8 @@ __global__ void __launch_bounds__(384, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.q_full[i], MODE == MODE_KEYS ? 8 : 4);
-      mbar_init(&ctl.s_full[i], 1);
+      mbar_init(&ctl.s_full[i][0], 1);
+      mbar_init(&ctl.s_full[i][1], 1);
       mbar_init(&ctl.p_full[i][0], 4);
       mbar_init(&ctl.p_full[i][1], 4);
       mbar_init(&ctl.o_full[i], 1);
@@ -295,8 +336,8 @@ __global__ void __launch_bounds__(384, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = ctl.tmem;
-  constexpr uint32_t O_COL = 256;
+  // All 512 columns are this CTA's: its tensor memory begins at address 0.
+  constexpr uint32_t tmem = 0, O_COL = 256;
 
   Walk<MODE, C::ROWS> walk;
   Unit u;
@@ -306,14 +347,23 @@ __global__ void __launch_bounds__(384, 1)
   if (warp < 8) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------------------- softmax
-    const int st = warp / 4, tid = threadIdx.x & 127;  // stream; row of its tile
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // TMEM lane base of the warp
-    const uint32_t s_tm = tmem + lanes + 128 * st, o_tm = tmem + lanes + O_COL + HD * st;
+    const int st = warp / 4, quad = warp & 3;     // stream; 32 rows
+    const int row = quad * 32 + lane;             // row of the stream's tile
+    const uint32_t lanes = (uint32_t)quad << 21;  // TMEM lane base of the warp
+    const uint32_t o_tm = tmem + lanes + O_COL + HD * st;
     const float c = fmaxf(fabsf(a.scale) * LOG2E, 1e-30f);
     constexpr float BIAS = std::is_same<T, __half>::value ? 6.f : 0.f;
     char *q_tile = base + (MODE == MODE_KEYS ? 0 : st) * C::TILE;
     const int row_off = MODE == MODE_KEYS ? 0 : 128 * st;  // first unit row of the tile
-    uint32_t ph_s = 0, ph_o = 0, ph_both = 0;
+    // A warp's share of a row's columns, for queries and outputs, in 16-byte pieces: the same
+    // bytes of the query tile in both.
+    constexpr int CW = HD / 8 / (MODE == MODE_KEYS ? 2 : 1);
+    const int ch0 = MODE == MODE_KEYS ? CW * st : 0;
+    auto piece = [&](int r, int ch) {  // K-major, 128-byte swizzle
+      return q_tile + (ch / 8) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
+    };
+    uint32_t ph_s = 0, ph_both = 0;  // ph_s: a bit per half
+    uint32_t n_pv = 0;               // products of the stream in earlier units: phases of o_full
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t &ph) {
       ok = __all_sync(0xffffffffu, mbar_wait(bar, ph, abort, WAIT_NS));
@@ -321,7 +371,7 @@ __global__ void __launch_bounds__(384, 1)
       ph ^= 1;
       return ok;
     };
-    // Both warpgroups have come here.
+    // All softmax warps have come here.
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.both);
@@ -329,38 +379,34 @@ __global__ void __launch_bounds__(384, 1)
     };
 
     while (ok && walk.next(a, u)) {
-      const int n_mine = stream_tiles<MODE>(a, u, st);
+      const int n_mine = stream_halves<MODE>(a, u, st);
       const int tile_rows = u.n_rows - row_off;  // rows of this stream's tile, may exceed 128
       const int64_t row_base = TREE ? 0 : u.base;
       const int entry = TREE ? u.b : 0;
+      const int pr = u.row0 + row_off + row;  // packed row, its token (tree: node) and its head
+      const int tok = pr / a.group;
+      const int64_t head = (int64_t)u.kvh * a.group + (pr - tok * a.group);
 
-      // Queries into shared memory: K-major, 128-byte swizzle; the scale's sign goes with them. (A
-      // stream without tiles skips the unit, so that it cannot run ahead of the MMA warp.)
+      // Queries into shared memory, with the scale's sign: every warp its columns of its 32 rows,
+      // all loads in flight at once; lane i holds row i's address. (A stream without tiles skips
+      // the unit, so that it cannot run ahead of the MMA warp.)
       if (MODE == MODE_KEYS || n_mine > 0) {
-        // Every warp its own 32 rows (in MODE_KEYS half of their columns), all loads in flight at
-        // once; lane i holds row i's address.
-        constexpr int CH = HD / 8, CW = MODE == MODE_KEYS ? CH / 2 : CH, N = CW;
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-        const int w0 = (warp & 3) * 32, pr = u.row0 + row_off + w0 + lane, tk = pr / a.group;
-        const uint64_t row_at = reinterpret_cast<uint64_t>(
-            static_cast<const T *>(a.q.data) +
-            at(a.q, entry, row_base + tk, (int64_t)u.kvh * a.group + (pr - tk * a.group)));
-        uint4 x[N];
+        const uint64_t row_at = reinterpret_cast<uint64_t>(static_cast<const T *>(a.q.data) +
+                                                           at(a.q, entry, row_base + tok, head));
+        uint4 x[CW];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = (32 * i + lane) / CW;
-          const int ch = lane % CW + (MODE == MODE_KEYS ? st * CW : 0);
+        for (int i = 0; i < CW; ++i) {
+          const int r = (32 * i + lane) / CW, ch = ch0 + lane % CW;
           const uint64_t src = __shfl_sync(0xffffffffu, row_at, r);
           x[i] = make_uint4(0, 0, 0, 0);
-          if (w0 + r < tile_rows && ch * 8 < a.head_dim)
+          if (quad * 32 + r < tile_rows && ch * 8 < a.head_dim)
             x[i] = *reinterpret_cast<const uint4 *>(src + ch * 16);
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int r = w0 + (32 * i + lane) / CW;
-          const int ch = lane % CW + (MODE == MODE_KEYS ? st * CW : 0);
-          *reinterpret_cast<uint4 *>(q_tile + (ch / 8) * 16384 + r * 128 +
-                                     (((ch & 7) ^ (r & 7)) * 16)) =
+        for (int i = 0; i < CW; ++i) {
+          const int r = (32 * i + lane) / CW, ch = ch0 + lane % CW;
+          *reinterpret_cast<uint4 *>(piece(quad * 32 + r, ch)) =
               make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
         }
         fence_proxy_async_smem();
@@ -368,44 +414,45 @@ __global__ void __launch_bounds__(384, 1)
         if (lane == 0) mbar_arrive(&ctl.q_full[MODE == MODE_KEYS ? 0 : st]);
       }
 
-      const int my_row = min(tid, tile_rows - 1);
-      const int pr = u.row0 + row_off + max(my_row, 0);
-      const int tok = pr / a.group;  // prompt: the row's token; tree: its node
-      const bool busy = (warp & 3) * 32 < tile_rows;  // the warp has a row
+      const bool busy = quad * 32 < tile_rows;  // the warp has a row
       uint32_t mask[4] = {0, 0, 0, 0};
       if constexpr (TREE) {
-        if (busy) node_mask(a, a.parents + (int64_t)u.b * a.nodes, tok, mask);
+        if (busy) node_mask(a, a.parents + (int64_t)u.b * a.nodes, min(tok, a.nodes - 1), mask);
       }
 
       float m = -INFINITY, l = 0.f;
       for (int i = 0; ok && i < n_mine; ++i) {
-        const int t = u.t0 + (MODE == MODE_KEYS ? 2 * i + st : i);
-        if (!wait(&ctl.s_full[st], ph_s)) break;
+        const int h = i & 1, t = u.t0 + (MODE == MODE_KEYS ? (i & ~1) + st : i >> 1);
+        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[st][h], ph_s >> h & 1, abort, WAIT_NS));
+        ph_s ^= 1u << h;
+        if (!ok) {
+          ctl.abort = 1;
+          break;
+        }
         fence_after_sync();
         if (busy) {
-          float s[128];
+          const uint32_t s_tm = tmem + lanes + 128 * st + 64 * h;
+          float s[64], top[4];
           tmem_ld32(s_tm, s);
           tmem_ld32(s_tm + 32, s + 32);
-          tmem_ld32(s_tm + 64, s + 64);
-          tmem_ld32(s_tm + 96, s + 96);
           tmem_ld_wait();
-          int r0, r1;
-          if (hidden_rows<MODE>(a, u, t, r0, r1)) {
+          if (hidden_from<MODE>(u, t) < 64 * h + 64) {
+            uint32_t see[2];
             if (!TREE || t < u.cache_tiles) {
-              const int lim = TREE ? u.len - 1 - t * KT : tok - t * KT;  // last visible column
-#pragma unroll
-              for (int j = 0; j < 128; ++j) s[j] = j <= lim ? s[j] : -INFINITY;
+              const int n = (TREE ? u.len : tok + 1) - t * KT - 64 * h;  // visible keys
+              see[0] = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+              see[1] = n <= 32 ? 0u : n >= 64 ? 0xffffffffu : (1u << (n - 32)) - 1u;
             } else {
-#pragma unroll
-              for (int j = 0; j < 128; ++j)
-                s[j] = mask[j / 32] >> (j % 32) & 1 ? s[j] : -INFINITY;
+              see[0] = h ? mask[2] : mask[0];
+              see[1] = h ? mask[3] : mask[1];
             }
+#pragma unroll
+            for (int j = 0; j < 64; ++j) s[j] = see[j / 32] >> (j % 32) & 1 ? s[j] : -INFINITY;
           }
-          float top[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) top[j] = fmaxf(s[j], s[j + 4]);
 #pragma unroll
-          for (int j = 8; j < 128; j += 8)
+          for (int j = 8; j < 64; j += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[j + e], s[j + e + 4]);
           const float mn = max3(max3(m, top[0], top[1]), top[2], top[3]);
@@ -414,8 +461,15 @@ __global__ void __launch_bounds__(384, 1)
             const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
             l *= f;
             m = mn;
-            // S(i) complete: so is the previous P V of this stream, which was issued before it
             if (i > 0) {
+              // The stream's previous product must have left O.
+              ok = __all_sync(0xffffffffu,
+                              mbar_wait(&ctl.o_full[st], (n_pv + i - 1) & 1, abort, WAIT_NS));
+              if (!ok) {
+                ctl.abort = 1;
+                break;
+              }
+              fence_after_sync();
 #pragma unroll 1
               for (int j = 0; j < HD / 16; ++j) {
                 float o[16];
@@ -429,159 +483,136 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           const float off = BIAS - (m == -INFINITY ? 0.f : m * c);
-          const float2 c2 = make_float2(c, c), off2 = make_float2(off, off);
           float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 2; ++j) {
             uint32_t p[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float2 x = fma2(make_float2(s[32 * j + 2 * e], s[32 * j + 2 * e + 1]), c2, off2);
-              if (e * POLY % 16 < POLY) {
-                x = poly_ex2<T>(x);
-              } else {
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-              }
-              sum[e & 1] = add2(sum[e & 1], x);
-              p[e] = pack2<T>(x.x, x.y);
-            }
+            weights<T>(s + 32 * j, c, off, sum, p);
             tmem_st16(s_tm + 16 * j, p);
-            if (j == 1) {  // the second product starts on the first half
-              tmem_st_wait();
-              fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&ctl.p_full[st][0]);
-            }
           }
           l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
           tmem_st_wait();
           fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.p_full[st][1]);
-        } else if (lane == 0) {
-          mbar_arrive(&ctl.p_full[st][0]);
-          mbar_arrive(&ctl.p_full[st][1]);
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl.p_full[st][h]);
       }
       if (!ok) break;
 
-      // Epilogue.
-      if (n_mine > 0 && !wait(&ctl.o_full[st], ph_o)) break;
+      // Epilogue. All products of the stream are complete, its query tile is idle.
+      if (n_mine > 0) {
+        // The last two products, in order (a parity says nothing before the phase it follows is
+        // over); those before them were complete when the last S was.
+        n_pv += n_mine;
+        ok = __all_sync(0xffffffffu,
+                        (n_mine < 2 ||
+                         mbar_wait(&ctl.o_full[st], (n_pv - 2) & 1, abort, WAIT_NS)) &&
+                            mbar_wait(&ctl.o_full[st], (n_pv - 1) & 1, abort, WAIT_NS));
+        if (!ok) {
+          ctl.abort = 1;
+          break;
+        }
+      }
       float w[2] = {0.f, 0.f};  // weights of the two streams' O
-      int c0 = 0, c1 = HD;      // this thread's columns
       float ml = m == -INFINITY ? -INFINITY : m * c;
+      const bool two = MODE == MODE_KEYS && stream_halves<MODE>(a, u, 1) > 0;
       if constexpr (MODE == MODE_KEYS) {
-        // The query tile is idle once both streams' products are complete.
+        float *stat = reinterpret_cast<float *>(&ctl + 1);
+        stat[2 * st * 128 + row] = ml;
+        stat[(2 * st + 1) * 128 + row] = l;
         if (!meet()) break;
-        float *stat = reinterpret_cast<float *>(base);
-        stat[(2 * st) * 128 + tid] = ml;
-        stat[(2 * st + 1) * 128 + tid] = l;
-        if (!meet()) break;
-        const float m0 = stat[tid], l0 = stat[128 + tid], m1 = stat[256 + tid],
-                    l1 = stat[384 + tid];
-        if (!meet()) break;  // the statistics' place is free again
+        const float m0 = stat[row], m1 = stat[256 + row];
         ml = fmaxf(m0, m1);
         const float ref = ml == -INFINITY ? 0.f : ml;
         w[0] = ex2(m0 - ref);
         w[1] = ex2(m1 - ref);
-        l = l0 * w[0] + (stream_tiles<MODE>(a, u, 1) > 0 ? l1 * w[1] : 0.f);
-        c0 = HD / 2 * st;
-        c1 = c0 + HD / 2;
+        l = stat[128 + row] * w[0] + (two ? stat[384 + row] * w[1] : 0.f);
       }
       fence_after_sync();
-      const bool two = MODE == MODE_KEYS && stream_tiles<MODE>(a, u, 1) > 0;
       const bool fix = *(volatile int *)&ctl.fix[walk.count & 7] == walk.count;
       const bool whole = !TREE || (u.t0 == 0 && u.t1 == u.n_tiles);
-      const bool mine = tid < tile_rows;
+      const bool mine = row < tile_rows;
       const bool live = !TREE || (mask[0] | mask[1] | mask[2] | mask[3]);
       if (busy) {
         const uint32_t o0 = tmem + lanes + O_COL;
         const float inv = 1.f / l;
         const bool zero = l == 0.f || !live;
-        char *stage = q_tile + (size_t)tid * HD * 2;
         float *slot = static_cast<float *>(a.ws) +
                       (2 * blockIdx.x + (u.t0 > 0 ? 0 : 1)) * dense_slot_floats(C::ROWS, HD);
 #pragma unroll 1
-        for (int col = c0; col < c1; col += 32) {
-          float o[32];
+        for (int ch = ch0; ch < ch0 + CW; ch += 2) {
+          const int col = ch * 8;
+          float o[16];
           if constexpr (MODE == MODE_KEYS) {
-            float o1[32];
-            tmem_ld32(o0 + col, o);
-            tmem_ld32(o0 + HD + col, o1);
+            float o1[16];
+            tmem_ld16(o0 + col, o);
+            tmem_ld16(o0 + HD + col, o1);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = two ? o[e] * w[0] + o1[e] * w[1] : o[e] * w[0];
+            for (int e = 0; e < 16; ++e) o[e] = two ? o[e] * w[0] + o1[e] * w[1] : o[e] * w[0];
           } else {
-            tmem_ld32(o_tm + col, o);
+            tmem_ld16(o_tm + col, o);
             tmem_ld_wait();
           }
-          if (fix && mine) {
+          if (fix && mine && (!TREE || u.t1 > u.cache_tiles)) {
             // Values that were replaced by zero, for the rows that see them.
             const int lo = TREE ? 0 : first_token(a, u) + 1, hi = TREE ? a.nodes : tok + 1;
-            if (!TREE || u.t1 > u.cache_tiles) {
-              const T *v = static_cast<const T *>(a.v.data) + at(a.v, entry, row_base, u.kvh);
-              for (int j = lo; j < hi; ++j) {
-                if (TREE && !((j < 64 ? j < 32 ? mask[0] : mask[1] : j < 96 ? mask[2] : mask[3]) >>
-                              (j & 31) & 1))
-                  continue;
+            const T *v = static_cast<const T *>(a.v.data) + at(a.v, entry, row_base, u.kvh) + col;
+            for (int j = lo; j < hi; ++j) {
+              if (TREE && !((j < 64 ? j < 32 ? mask[0] : mask[1] : j < 96 ? mask[2] : mask[3]) >>
+                            (j & 31) & 1))
+                continue;
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                  if (col + e >= a.head_dim) break;
-                  const T x = v[j * a.v.row + col + e];
-                  if (!finite_bits(x)) o[e] += to_f(x);
-                }
+              for (int e = 0; e < 16; ++e) {
+                if (col + e >= a.head_dim) break;
+                const T x = v[j * a.v.row + e];
+                if (!finite_bits(x)) o[e] += to_f(x);
               }
             }
           }
           if (whole) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = zero ? 0.f : o[e] * inv;
+            for (int e = 0; e < 16; ++e) o[e] = zero ? 0.f : o[e] * inv;
 #pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
-              const int ch = col / 8 + q4;
-              *reinterpret_cast<uint4 *>(stage + ((ch ^ (tid & 7)) * 16)) = make_uint4(
-                  pack2<T>(o[8 * q4], o[8 * q4 + 1]), pack2<T>(o[8 * q4 + 2], o[8 * q4 + 3]),
-                  pack2<T>(o[8 * q4 + 4], o[8 * q4 + 5]), pack2<T>(o[8 * q4 + 6], o[8 * q4 + 7]));
-            }
+            for (int h = 0; h < 2; ++h)
+              *reinterpret_cast<uint4 *>(piece(row, ch + h)) = make_uint4(
+                  pack2<T>(o[8 * h], o[8 * h + 1]), pack2<T>(o[8 * h + 2], o[8 * h + 3]),
+                  pack2<T>(o[8 * h + 4], o[8 * h + 5]), pack2<T>(o[8 * h + 6], o[8 * h + 7]));
           } else if (mine) {
 #pragma unroll
-            for (int q4 = 0; q4 < 8; ++q4)
-              reinterpret_cast<float4 *>(slot)[(size_t)(col / 4 + q4) * C::ROWS + row_off + tid] =
-                  make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
+            for (int h = 0; h < 4; ++h)
+              reinterpret_cast<float4 *>(slot)[(size_t)(col / 4 + h) * C::ROWS + row_off + row] =
+                  make_float4(o[4 * h], o[4 * h + 1], o[4 * h + 2], o[4 * h + 3]);
           }
         }
         if (!whole) {
-          if (mine && (MODE != MODE_KEYS || st == 0)) {
-            slot[(size_t)C::ROWS * HD + row_off + tid] = ml;
-            slot[(size_t)C::ROWS * (HD + 1) + row_off + tid] = l;
+          if (mine && ch0 == 0) {  // padding nodes: a part that saw nothing
+            slot[(size_t)C::ROWS * HD + row_off + row] = live ? ml : -INFINITY;
+            slot[(size_t)C::ROWS * (HD + 1) + row_off + row] = live ? l : 0.f;
           }
         } else {
-          // Whole rows leave in coalesced 16-byte pieces, the warp's own 32 rows.
+          // Whole rows leave in coalesced 16-byte pieces.
           __syncwarp();
-          T *out = static_cast<T *>(a.out.data) +
-                   at(a.out, entry, row_base + pr / a.group,
-                      (int64_t)u.kvh * a.group + pr % a.group);
-          const int n_rows = min(32, tile_rows - (warp & 3) * 32);
-          constexpr int CN = HD / 8 / (MODE == MODE_KEYS ? 2 : 1);
-          const int ch = lane % CN + c0 / 8;
+          const uint64_t out = reinterpret_cast<uint64_t>(static_cast<T *>(a.out.data) +
+                                                          at(a.out, entry, row_base + tok, head));
+          const int ch = ch0 + lane % CW;
 #pragma unroll
-          for (int i = 0; i < CN; ++i) {
-            const int r = (32 * i + lane) / CN, rr = (warp & 3) * 32 + r;
-            const uint64_t dst = __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), r);
-            if (r < n_rows && ch * 8 < a.head_dim)
-              *reinterpret_cast<uint4 *>(dst + ch * 16) = *reinterpret_cast<const uint4 *>(
-                  q_tile + (size_t)rr * HD * 2 + ((ch ^ (rr & 7)) * 16));
+          for (int i = 0; i < CW; ++i) {
+            const int r = (32 * i + lane) / CW;
+            const uint64_t dst = __shfl_sync(0xffffffffu, out, r);
+            if (quad * 32 + r < tile_rows && ch * 8 < a.head_dim)
+              *reinterpret_cast<uint4 *>(dst + ch * 16) =
+                  *reinterpret_cast<const uint4 *>(piece(quad * 32 + r, ch));
           }
+          __syncwarp();
         }
       }
       fence_before_sync();
-      // The query tile and both O are read by both warpgroups: neither goes on before the other.
+      // Both O and the statistics are read by both streams: neither goes on before the other.
       if constexpr (MODE == MODE_KEYS) {
         if (!meet()) break;
         fence_after_sync();
       }
-      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
@@ -610,8 +641,7 @@ __global__ void __launch_bounds__(384, 1)
           const int row = TREE ? (cache ? t : t - u.cache_tiles) * KT : (int)u.base + t * KT;
           const uint32_t dst = ring_smem + pos.slot * C::TILE;
           mbar_arrive_expect_tx(&ctl.kv_full[pos.slot], C::TILE);
-          int r0, r1;
-          if (value && hidden_rows<MODE>(a, u, t, r0, r1)) mbar_arrive(&ctl.v_req[pos.slot]);
+          if (value && hidden_from<MODE>(u, t) < KT) mbar_arrive(&ctl.v_req[pos.slot]);
           for (int s = 0; s < C::SLABS; ++s)
             tma_load_4d(dst + s * 16384, map, s * 64, head, row, entry, &ctl.kv_full[pos.slot]);
           ++issued;
@@ -640,96 +670,138 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------------------------- MMAs
-    constexpr uint32_t ID_S = idesc<T>(128, KT, false), ID_O = idesc<T>(128, HD, true);
+    // The whole warp walks through the loops in step and one lane issues: addresses and descriptors
+    // then stay in uniform registers, which is where the MMA takes them from (with a single lane in
+    // the loops every MMA paid for the moves: 75 clocks each, and 800 between a P and the next).
+    constexpr uint32_t ID_S = idesc<T>(128, KT / 2, false), ID_O = idesc<T>(128, HD, true);
+    const uint32_t leader = elect_one();
     RingPos pos;
-    uint32_t ph_q[2] = {0, 0}, ph_v = 0, ph_p[2] = {0, 0};  // ph_v: a bit per slot
+    uint32_t ph_q[2] = {0, 0}, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per stream, half
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t ph) {
-      if (ok && !mbar_wait(bar, ph, abort, WAIT_NS)) {
-        ok = false;
-        ctl.abort = 1;
-      }
+      ok = __all_sync(0xffffffffu, mbar_wait(bar, ph & 1, abort, WAIT_NS));
+      if (!ok) ctl.abort = 1;
       return ok;
     };
-    auto scores = [&](int s, uint32_t k_tile) {
+    auto tile_at = [&](const RingPos &p) { return ring_smem + p.slot * C::TILE; };
+    // S of stream s over half h of a key tile.
+    auto scores = [&](int s, int h, const RingPos &kp) {
       const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : s) * C::TILE);
-      const uint64_t kd = sw128_desc(k_tile);
+      const uint64_t kd = sw128_desc(tile_at(kp) + h * 8192);
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k) {
         const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        mma_bf16(tmem + 128 * s, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
+        mma_ss(leader, tmem + 128 * s + 64 * h, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
       }
-      mma_commit(&ctl.s_full[s]);
+      commit(leader, &ctl.s_full[s][h]);
     };
-    // P V over the keys of one half.
-    auto values = [&](int s, int half, uint32_t v_tile, bool first) {
-      const uint64_t vd = desc_add(sw128_mn_desc(v_tile, 16384), half * 8192);
-      const uint32_t p = tmem + 128 * s + 32 * half;
+    // P V of stream s over half h of a value tile, once its softmax has written P.
+    auto values = [&](int s, int h, const RingPos &vp, bool first) {
+      if (!wait(&ctl.p_full[s][h], ph_p >> (2 * s + h))) return;
+      ph_p ^= 1u << (2 * s + h);
+      fence_after_sync();
+      const uint64_t vd = sw128_mn_desc(tile_at(vp) + h * 8192, 16384);
 #pragma unroll
       for (int k = 0; k < KT / 32; ++k)
-        mma_bf16_ts(tmem + O_COL + HD * s, p + 8 * k, desc_add(vd, k * 2048), ID_O,
-                    !first || half > 0 || k > 0);
+        mma_ts(leader, tmem + O_COL + HD * s, tmem + 128 * s + 64 * h + 8 * k,
+               desc_add(vd, k * 2048), ID_O, !first || k > 0);
+      commit(leader, &ctl.o_full[s]);
     };
+    auto value_tile = [&](int t, const RingPos &vp) {
+      if (!wait(&ctl.kv_full[vp.slot], vp.phase)) return;
+      if (hidden_from<MODE>(u, t) < KT) {
+        wait(&ctl.v_ok[vp.slot], ph_v >> vp.slot);
+        ph_v ^= 1u << vp.slot;
+      }
+    };
+    // Two S per stream: the next half's scores are under way while the softmax works on this
+    // half's. S(i + 2) goes where P(i) was, behind P(i) V(i) in the same pipe.
     while (ok && walk.next(a, u)) {
-      if (lane == 0) {
-        const int n = u.t1 - u.t0;
-        const int n_s[2] = {stream_tiles<MODE>(a, u, 0), stream_tiles<MODE>(a, u, 1)};
-        auto tile_at = [&](const RingPos &p) { return ring_smem + p.slot * C::TILE; };
-        for (int s = 0; s < (MODE == MODE_KEYS ? 1 : 2); ++s)
-          if (n_s[s] > 0) {
-            wait(&ctl.q_full[s], ph_q[s]);
-            ph_q[s] ^= 1;
-          }
-        for (int i = 0; i < C::AHEAD && i < n && ok; ++i) {
+      const int n = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0);
+      const int n0 = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, 0), 0);
+      const int n1 = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, 1), 0);
+#define N_S(s) ((s) ? n1 : n0)
+#pragma unroll
+      for (int s = 0; s < (MODE == MODE_KEYS ? 1 : 2); ++s)
+        if (ok && N_S(s) > 0) {
+          wait(&ctl.q_full[s], ph_q[s]);
+          ph_q[s] ^= 1;
+        }
+      fence_after_sync();
+      if constexpr (MODE == MODE_KEYS) {
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (s >= n || !ok) break;
           if (!wait(&ctl.kv_full[pos.slot], pos.phase)) break;
-          fence_after_sync();
-          for (int s = 0; s < 2; ++s)
-            if (MODE == MODE_KEYS ? s == i : n_s[s] > 0) scores(s, tile_at(pos));
-          mma_commit(&ctl.kv_empty[pos.slot]);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            if (h < N_S(s)) scores(s, h, pos);
+          commit(leader, &ctl.kv_empty[pos.slot]);
           pos.next(C::SLOTS);
         }
+        for (int i = 0; i < n && ok; i += 2) {
+          RingPos vp[2], kp[2];
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            vp[s] = kp[s] = pos;
+            if (i + s >= n) continue;
+            pos.next(C::SLOTS);
+            kp[s] = pos;
+            if (i + s + 2 < n) pos.next(C::SLOTS);
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (!ok || i + s >= n) break;
+              if (i + h < N_S(s)) {
+                if (h == 0) value_tile(u.t0 + i + s, vp[s]);
+                if (ok) values(s, h, vp[s], i + h == 0);
+                if (ok && i + h + 2 < N_S(s)) {
+                  if (h == 0) wait(&ctl.kv_full[kp[s].slot], kp[s].phase);
+                  if (ok) scores(s, h, kp[s]);
+                }
+              }
+              if (!ok || h == 0) continue;
+              commit(leader, &ctl.kv_empty[vp[s].slot]);
+              if (i + s + 2 < n) commit(leader, &ctl.kv_empty[kp[s].slot]);
+            }
+        }
+      } else {
+        if (ok) wait(&ctl.kv_full[pos.slot], pos.phase);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int s = 0; s < 2; ++s)
+            if (ok && h < N_S(s)) scores(s, h, pos);
+        commit(leader, &ctl.kv_empty[pos.slot]);
+        pos.next(C::SLOTS);
         for (int i = 0; i < n && ok; ++i) {
           const RingPos vp = pos;
           pos.next(C::SLOTS);
-          const bool more = i + C::AHEAD < n;
           const RingPos kp = pos;
+          const bool more = i + 1 < n;
           if (more) pos.next(C::SLOTS);
-          if (!wait(&ctl.kv_full[vp.slot], vp.phase)) break;
-          int r0, r1;
-          if (hidden_rows<MODE>(a, u, u.t0 + i, r0, r1)) {
-            if (!wait(&ctl.v_ok[vp.slot], ph_v >> vp.slot & 1)) break;
-            ph_v ^= 1u << vp.slot;
-          }
-          bool have_k = false;
-          for (int s = 0; s < 2; ++s) {
-            const int mine = MODE == MODE_KEYS ? i / 2 : i;  // the stream's tile number
-            if (MODE == MODE_KEYS ? (i & 1) != s : i >= n_s[s]) continue;
-            if (!wait(&ctl.p_full[s][0], ph_p[s])) break;
-            fence_after_sync();
-            values(s, 0, tile_at(vp), mine == 0);
-            if (!wait(&ctl.p_full[s][1], ph_p[s])) break;
-            ph_p[s] ^= 1;
-            fence_after_sync();
-            values(s, 1, tile_at(vp), mine == 0);
-            if (mine == n_s[s] - 1) mma_commit(&ctl.o_full[s]);
-            if (MODE == MODE_KEYS) mma_commit(&ctl.kv_empty[vp.slot]);
-            if (mine + 1 < n_s[s]) {
-              if (!have_k && !wait(&ctl.kv_full[kp.slot], kp.phase)) break;
-              have_k = true;
-              fence_after_sync();
-              scores(s, tile_at(kp));
+          value_tile(u.t0 + i, vp);
+          if (ok && more) wait(&ctl.kv_full[kp.slot], kp.phase);
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (!ok || 2 * i + h >= N_S(s)) continue;
+              values(s, h, vp, 2 * i + h == 0);
+              if (ok && 2 * i + h + 2 < N_S(s)) scores(s, h, kp);
             }
-          }
           if (!ok) break;
-          if (MODE != MODE_KEYS) mma_commit(&ctl.kv_empty[vp.slot]);
-          if (more) mma_commit(&ctl.kv_empty[kp.slot]);
+          commit(leader, &ctl.kv_empty[vp.slot]);
+          if (more) commit(leader, &ctl.kv_empty[kp.slot]);
         }
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+#undef N_S
     }
     // Every MMA and commit has completed before the CTA gives its tensor memory back.
+    commit(leader, &ctl.drain);
     if (lane == 0) {
-      mma_commit(&ctl.drain);
       const uint64_t t0 = globaltimer();
       while (!mbar_try_wait(&ctl.drain, 0) && globaltimer() - t0 < WAIT_NS) {
       }
@@ -745,8 +817,9 @@ __global__ void __launch_bounds__(384, 1)
       for (int i = 0; i < C::AHEAD && i < n; ++i) pos.next(C::SLOTS);
       for (int i = 0; i < n && ok; ++i) {
         const int t = u.t0 + i;
-        int r0, r1;
-        if (hidden_rows<MODE>(a, u, t, r0, r1)) {
+        const int r0 = max(0, hidden_from<MODE>(u, t));
+        const int r1 = !TREE || t < u.cache_tiles ? KT : a.nodes;
+        if (r0 < KT) {
           ok = __all_sync(0xffffffffu,
                           mbar_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort, WAIT_NS) &&
                               mbar_wait(&ctl.kv_full[pos.slot], pos.phase, abort, WAIT_NS));
