@@ -46,7 +46,6 @@ constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;  // log2 of the growth of a row's maximum that is left in P
 enum { MODE_PROMPT = 0, MODE_ROWS = 1, MODE_KEYS = 2 };
 constexpr int MAX_SLOTS = 8;
-constexpr int POLY = 0;  // of 16 exponentials, how many take the FMA pipe
 
 struct Maps {
   CUtensorMap k, v, kc, vc;  // kc, vc: tree
@@ -116,12 +115,6 @@ ISKV_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-ISKV_DEV float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 template <typename T>
 ISKV_DEV uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -132,59 +125,17 @@ ISKV_DEV uint32_t pack2(float a, float b) {
   }
 }
 
-// The weights 2^(s c + off) of 32 scores, in place, as 16 packed pairs, and their sum. POLY of the 16
-// pairs take the FMA pipe (the exponential unit's 16 a clock are not enough for both streams):
-// x = n + f, n the nearest integer: adding 1.5 2^23 + 127 leaves n + 127 in the low bits, which
-// shifted by 23 are the float 2^n (0 for n = -127); 2^f is a polynomial with p(0) = 1, fitted for
-// the smallest largest relative error on [-1/2, 1/2]: degree 3, 1.0e-4, for bf16 (half a step of P
-// is 3.9e-3), degree 4, 2.8e-6, for fp16 (4.9e-4). x <= 14; -inf gives 0, NaN stays NaN.
-// Step by step over all pairs, so that no instruction waits for the one before it.
+// The weights 2^(s c + off) of 32 scores as 16 packed pairs, added to sum.
 template <typename T>
-ISKV_DEV void weights(float *s, float c, float off, float2 (&sum)[2], uint32_t (&p)[16]) {
-  constexpr float MAGIC = 12582912.f + 127.f;
-  constexpr bool H = std::is_same<T, __half>::value;
-  auto both = [](float v) { return make_float2(v, v); };
-  auto poly = [](int e) { return e * POLY % 16 < POLY; };
-  float2 x[16], r[16], q[16];
-#pragma unroll
-  for (int e = 0; e < 16; ++e) x[e] = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), both(c), both(off));
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e)) {
-      x[e] = make_float2(max_nan(x[e].x, -127.f), max_nan(x[e].y, -127.f));
-      r[e] = __fadd2_rn(x[e], both(MAGIC));
-    } else {
-      x[e].x = ex2(x[e].x);
-      x[e].y = ex2(x[e].y);
-    }
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e)) x[e] = __fadd2_rn(x[e], __ffma2_rn(r[e], both(-1.f), both(MAGIC)));
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e))
-      q[e] = H ? __ffma2_rn(both(0.009582853f), x[e], both(0.055906426f))
-               : __ffma2_rn(both(0.055008933f), x[e], both(0.24221095f));
-  if constexpr (H) {
-#pragma unroll
-    for (int e = 0; e < 16; ++e)
-      if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(0.24024099f));
-  }
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(H ? 0.69312418f : 0.6932829f));
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e)) q[e] = __ffma2_rn(q[e], x[e], both(1.f));
-#pragma unroll
-  for (int e = 0; e < 16; ++e)
-    if (poly(e))
-      x[e] = __fmul2_rn(q[e], make_float2(__int_as_float(__float_as_int(r[e].x) << 23),
-                                    __int_as_float(__float_as_int(r[e].y) << 23)));
+ISKV_DEV void weights(const float *s, float c, float off, float2 (&sum)[2], uint32_t (&p)[16]) {
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
-    sum[e & 1] = __fadd2_rn(sum[e & 1], x[e]);
-    p[e] = pack2<T>(x[e].x, x[e].y);
+    float2 x = __ffma2_rn(make_float2(s[2 * e], s[2 * e + 1]), make_float2(c, c),
+                          make_float2(off, off));
+    x.x = ex2(x.x);
+    x.y = ex2(x.y);
+    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+    p[e] = pack2<T>(x.x, x.y);
   }
 }
 
@@ -256,6 +207,35 @@ ISKV_DEV int stream_halves(const DenseArgs &a, const Unit &u, int s) {
 template <int MODE>
 ISKV_DEV int hidden_from(const Unit &u, int t) {
   return MODE == MODE_PROMPT || t < u.cache_tiles ? u.open - t * KT : 0;
+}
+
+// Whole warp: wait for the phase of the given parity; false after WAIT_NS or once another warp gave
+// up (the same for all lanes). The clock is read every 64th try only.
+ISKV_DEV bool warp_try(uint64_t *bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "vote.sync.all.pred p, p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return r != 0;
+}
+ISKV_DEV bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort) {
+  if (warp_try(bar, parity)) return true;
+  uint64_t t0 = 0;
+  for (int i = 1;; ++i) {
+    if (warp_try(bar, parity)) return true;
+    if (i % 64) continue;
+    const uint64_t t = __shfl_sync(0xffffffffu, globaltimer(), 0);
+    if (t0 == 0) t0 = t;
+    if (__any_sync(0xffffffffu, *abort != 0 || t - t0 > WAIT_NS)) {
+      *abort = 1;
+      return false;
+    }
+  }
 }
 
 // One lane of the warp (all lanes ask): 1 for it, 0 for the others.
@@ -365,17 +345,13 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t ph_s = 0, ph_both = 0;  // ph_s: a bit per half
     uint32_t n_pv = 0;               // products of the stream in earlier units: phases of o_full
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t &ph) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar, ph, abort, WAIT_NS));
-      if (!ok) ctl.abort = 1;
-      ph ^= 1;
-      return ok;
-    };
     // All softmax warps have come here.
     auto meet = [&]() {
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl.both);
-      return wait(&ctl.both, ph_both);
+      ok = warp_wait(&ctl.both, ph_both, abort);
+      ph_both ^= 1;
+      return ok;
     };
 
     while (ok && walk.next(a, u)) {
@@ -420,15 +396,12 @@ __global__ void __launch_bounds__(384, 1)
         if (busy) node_mask(a, a.parents + (int64_t)u.b * a.nodes, min(tok, a.nodes - 1), mask);
       }
 
-      float m = -INFINITY, l = 0.f;
-      for (int i = 0; ok && i < n_mine; ++i) {
-        const int h = i & 1, t = u.t0 + (MODE == MODE_KEYS ? (i & ~1) + st : i >> 1);
-        ok = __all_sync(0xffffffffu, mbar_wait(&ctl.s_full[st][h], ph_s >> h & 1, abort, WAIT_NS));
+      // m: the reference maximum; past top_lim it moves; off = BIAS - m c.
+      float m = -INFINITY, l = 0.f, top_lim = -INFINITY, off = BIAS;
+      auto step = [&](auto half, int i) {
+        constexpr int h = decltype(half)::value;
+        if (!warp_wait(&ctl.s_full[st][h], ph_s >> h & 1, abort)) return false;
         ph_s ^= 1u << h;
-        if (!ok) {
-          ctl.abort = 1;
-          break;
-        }
         fence_after_sync();
         if (busy) {
           const uint32_t s_tm = tmem + lanes + 128 * st + 64 * h;
@@ -436,6 +409,7 @@ __global__ void __launch_bounds__(384, 1)
           tmem_ld32(s_tm, s);
           tmem_ld32(s_tm + 32, s + 32);
           tmem_ld_wait();
+          const int t = u.t0 + (MODE == MODE_KEYS ? i - h + st : i / 2);
           if (hidden_from<MODE>(u, t) < 64 * h + 64) {
             uint32_t see[2];
             if (!TREE || t < u.cache_tiles) {
@@ -443,8 +417,8 @@ __global__ void __launch_bounds__(384, 1)
               see[0] = n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u;
               see[1] = n <= 32 ? 0u : n >= 64 ? 0xffffffffu : (1u << (n - 32)) - 1u;
             } else {
-              see[0] = h ? mask[2] : mask[0];
-              see[1] = h ? mask[3] : mask[1];
+              see[0] = mask[2 * h];
+              see[1] = mask[2 * h + 1];
             }
 #pragma unroll
             for (int j = 0; j < 64; ++j) s[j] = see[j / 32] >> (j % 32) & 1 ? s[j] : -INFINITY;
@@ -455,20 +429,16 @@ __global__ void __launch_bounds__(384, 1)
           for (int j = 8; j < 64; j += 8)
 #pragma unroll
             for (int e = 0; e < 4; ++e) top[e] = max3(top[e], s[j + e], s[j + e + 4]);
-          const float mn = max3(max3(m, top[0], top[1]), top[2], top[3]);
-          const bool grow = mn > m && (m == -INFINITY || (mn - m) * c > LAZY);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float f = mn == -INFINITY ? 1.f : ex2((m - mn) * c);
+          const float mn = max3(fmaxf(top[0], top[1]), top[2], top[3]);
+          if (__any_sync(0xffffffffu, mn > top_lim)) {
+            const float to = fmaxf(m, mn), f = to == -INFINITY ? 1.f : ex2((m - to) * c);
             l *= f;
-            m = mn;
+            m = to;
+            off = BIAS - (m == -INFINITY ? 0.f : m * c);
+            top_lim = m + LAZY / c;
             if (i > 0) {
               // The stream's previous product must have left O.
-              ok = __all_sync(0xffffffffu,
-                              mbar_wait(&ctl.o_full[st], (n_pv + i - 1) & 1, abort, WAIT_NS));
-              if (!ok) {
-                ctl.abort = 1;
-                break;
-              }
+              if (!warp_wait(&ctl.o_full[st], (n_pv + i - 1) & 1, abort)) return false;
               fence_after_sync();
 #pragma unroll 1
               for (int j = 0; j < HD / 16; ++j) {
@@ -482,20 +452,26 @@ __global__ void __launch_bounds__(384, 1)
               }
             }
           }
-          const float off = BIAS - (m == -INFINITY ? 0.f : m * c);
-          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             uint32_t p[16];
             weights<T>(s + 32 * j, c, off, sum, p);
             tmem_st16(s_tm + 16 * j, p);
           }
-          l += sum[0].x + sum[0].y + sum[1].x + sum[1].y;
+          sum[0] = __fadd2_rn(sum[0], sum[1]);
+          l = sum[0].x + sum[0].y;
           tmem_st_wait();
           fence_before_sync();
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl.p_full[st][h]);
+        return true;
+      };
+      for (int i = 0; i < n_mine; i += 2) {
+        ok = step(std::integral_constant<int, 0>{}, i);
+        if (ok && i + 1 < n_mine) ok = step(std::integral_constant<int, 1>{}, i + 1);
+        if (!ok) break;
       }
       if (!ok) break;
 
@@ -504,14 +480,9 @@ __global__ void __launch_bounds__(384, 1)
         // The last two products, in order (a parity says nothing before the phase it follows is
         // over); those before them were complete when the last S was.
         n_pv += n_mine;
-        ok = __all_sync(0xffffffffu,
-                        (n_mine < 2 ||
-                         mbar_wait(&ctl.o_full[st], (n_pv - 2) & 1, abort, WAIT_NS)) &&
-                            mbar_wait(&ctl.o_full[st], (n_pv - 1) & 1, abort, WAIT_NS));
-        if (!ok) {
-          ctl.abort = 1;
-          break;
-        }
+        ok = (n_mine < 2 || warp_wait(&ctl.o_full[st], (n_pv - 2) & 1, abort)) &&
+             warp_wait(&ctl.o_full[st], (n_pv - 1) & 1, abort);
+        if (!ok) break;
       }
       float w[2] = {0.f, 0.f};  // weights of the two streams' O
       float ml = m == -INFINITY ? -INFINITY : m * c;
@@ -679,8 +650,7 @@ __global__ void __launch_bounds__(384, 1)
     uint32_t ph_q[2] = {0, 0}, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per stream, half
     bool ok = true;
     auto wait = [&](uint64_t *bar, uint32_t ph) {
-      ok = __all_sync(0xffffffffu, mbar_wait(bar, ph & 1, abort, WAIT_NS));
-      if (!ok) ctl.abort = 1;
+      ok = warp_wait(bar, ph & 1, abort);
       return ok;
     };
     auto tile_at = [&](const RingPos &p) { return ring_smem + p.slot * C::TILE; };
@@ -820,9 +790,8 @@ __global__ void __launch_bounds__(384, 1)
         const int r0 = max(0, hidden_from<MODE>(u, t));
         const int r1 = !TREE || t < u.cache_tiles ? KT : a.nodes;
         if (r0 < KT) {
-          ok = __all_sync(0xffffffffu,
-                          mbar_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort, WAIT_NS) &&
-                              mbar_wait(&ctl.kv_full[pos.slot], pos.phase, abort, WAIT_NS));
+          ok = warp_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort) &&
+               warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
           ph_req ^= 1u << pos.slot;
           if (!ok) {
             ctl.abort = 1;
