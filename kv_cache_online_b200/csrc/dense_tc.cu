@@ -20,9 +20,10 @@
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row; P goes back to tensor memory in S's
 // place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring;
-// 9 issues the MMAs; 10-11 look through value tiles of which some row must not see some key, and replace what is not finite by zero before the MMA
-// reads it (0 * NaN would reach every row); if such a value is seen by some row, the epilogue adds
-// it to exactly the rows that see it.
+// 9 and 10 issue the MMAs of stream 0 and 1; 11 looks through value tiles of which some row must not
+// see some key, and replaces what is not finite by zero before the MMA reads it (0 * NaN would reach
+// every row); if such a value is seen by some row, the epilogue adds it to exactly the rows that
+// see it.
 //
 // Tensor memory (512 columns): two S of 128 x 64 per stream at 0 and 128 (P over the first half of
 // each), O0, O1 at 256.
@@ -59,7 +60,9 @@ struct Ctl {
   // says nothing about it), the check has passed it. A phase each per checked use of the slot, which
   // is not refilled before the MMA has read it.
   uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2];  // [stream][half of the tile's keys]
+  uint64_t q_full[2], s_full[2][2], p_full[2][2];  // [stream][half of the tile's keys]
+  uint64_t o_full[2];      // a phase per product P V; read only where the one before is known complete
+  uint64_t o_last[2];      // a phase per unit: its last P V
   uint64_t both, drain;
   uint32_t tmem;
   int abort;
@@ -293,9 +296,9 @@ __global__ void __launch_bounds__(384, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(&ctl.kv_full[i], 1);
-      mbar_init(&ctl.kv_empty[i], 1);
+      mbar_init(&ctl.kv_empty[i], 2);
       mbar_init(&ctl.v_req[i], 1);
-      mbar_init(&ctl.v_ok[i], 2);
+      mbar_init(&ctl.v_ok[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl.q_full[i], MODE == MODE_KEYS ? 8 : 4);
@@ -304,9 +307,10 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(&ctl.p_full[i][0], 4);
       mbar_init(&ctl.p_full[i][1], 4);
       mbar_init(&ctl.o_full[i], 1);
+      mbar_init(&ctl.o_last[i], 1);
     }
     mbar_init(&ctl.both, 8);
-    mbar_init(&ctl.drain, 1);
+    mbar_init(&ctl.drain, 2);
     ctl.abort = 0;
     for (int i = 0; i < 8; ++i) ctl.fix[i] = 0;
     fence_barrier_init();
@@ -342,7 +346,7 @@ __global__ void __launch_bounds__(384, 1)
     auto piece = [&](int r, int ch) {  // K-major, 128-byte swizzle
       return q_tile + (ch / 8) * 16384 + r * 128 + (((ch & 7) ^ (r & 7)) * 16);
     };
-    uint32_t ph_s = 0, ph_both = 0;  // ph_s: a bit per half
+    uint32_t ph_s = 0, ph_o = 0, ph_both = 0;  // ph_s: a bit per half
     uint32_t n_pv = 0;               // products of the stream in earlier units: phases of o_full
     bool ok = true;
     // All softmax warps have come here.
@@ -437,7 +441,8 @@ __global__ void __launch_bounds__(384, 1)
             off = BIAS - (m == -INFINITY ? 0.f : m * c);
             top_lim = m + LAZY / c;
             if (i > 0) {
-              // The stream's previous product must have left O.
+              // The stream's previous product must have left O. (The one before it has: S(i) was
+              // issued behind it. The next one waits for this warp.)
               if (!warp_wait(&ctl.o_full[st], (n_pv + i - 1) & 1, abort)) return false;
               fence_after_sync();
 #pragma unroll 1
@@ -477,11 +482,9 @@ __global__ void __launch_bounds__(384, 1)
 
       // Epilogue. All products of the stream are complete, its query tile is idle.
       if (n_mine > 0) {
-        // The last two products, in order (a parity says nothing before the phase it follows is
-        // over); those before them were complete when the last S was.
         n_pv += n_mine;
-        ok = (n_mine < 2 || warp_wait(&ctl.o_full[st], (n_pv - 2) & 1, abort)) &&
-             warp_wait(&ctl.o_full[st], (n_pv - 1) & 1, abort);
+        ok = warp_wait(&ctl.o_last[st], ph_o, abort);
+        ph_o ^= 1;
         if (!ok) break;
       }
       float w[2] = {0.f, 0.f};  // weights of the two streams' O
@@ -639,135 +642,95 @@ __global__ void __launch_bounds__(384, 1)
         p.next(C::SLOTS);
       }
     }
-  } else if (warp == 9) {
+  } else if (warp < 11) {
     // ------------------------------------------------------------------------- MMAs
-    // The whole warp walks through the loops in step and one lane issues: addresses and descriptors
-    // then stay in uniform registers, which is where the MMA takes them from (with a single lane in
-    // the loops every MMA paid for the moves: 75 clocks each, and 800 between a P and the next).
+    // A warp per stream: what it takes to see that a P has come and to issue the next products is
+    // longer than the products, and two warps overlap it (one warp for both: 1,740 clocks for 64
+    // keys of both streams at head_dim 128). The whole warp walks through the loops in step and one
+    // lane issues: addresses and descriptors then stay in uniform registers, where the MMA takes
+    // them from. Both warps follow every ring slot, used or not, so that neither loses a phase.
     constexpr uint32_t ID_S = idesc<T>(128, KT / 2, false), ID_O = idesc<T>(128, HD, true);
+    const int st = warp - 9;
     const uint32_t leader = elect_one();
     RingPos pos;
-    uint32_t ph_q[2] = {0, 0}, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per stream, half
+    uint32_t ph_q = 0, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per half
     bool ok = true;
-    auto wait = [&](uint64_t *bar, uint32_t ph) {
-      ok = warp_wait(bar, ph & 1, abort);
-      return ok;
-    };
-    auto tile_at = [&](const RingPos &p) { return ring_smem + p.slot * C::TILE; };
-    // S of stream s over half h of a key tile.
-    auto scores = [&](int s, int h, const RingPos &kp) {
-      const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : s) * C::TILE);
-      const uint64_t kd = sw128_desc(tile_at(kp) + h * 8192);
+    const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : st) * C::TILE);
+    const uint32_t s_tm = 128 * st, o_tm = O_COL + HD * st;
+    auto tile_at = [&](int slot) { return ring_smem + slot * C::TILE; };
+    // S over half h of a key tile.
+    auto scores = [&](int h, int slot) {
+      const uint64_t kd = sw128_desc(tile_at(slot) + h * 8192);
 #pragma unroll
       for (int k = 0; k < HD / 16; ++k) {
         const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        mma_ss(leader, tmem + 128 * s + 64 * h, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
+        mma_ss(leader, s_tm + 64 * h, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
       }
-      commit(leader, &ctl.s_full[s][h]);
+      commit(leader, &ctl.s_full[st][h]);
     };
-    // P V of stream s over half h of a value tile, once its softmax has written P.
-    auto values = [&](int s, int h, const RingPos &vp, bool first) {
-      if (!wait(&ctl.p_full[s][h], ph_p >> (2 * s + h))) return;
-      ph_p ^= 1u << (2 * s + h);
+    // P V over half h of a value tile, once the softmax has written P.
+    auto values = [&](int h, int slot, bool first, bool last) {
+      if (!warp_wait(&ctl.p_full[st][h], ph_p >> h & 1, abort)) return false;
+      ph_p ^= 1u << h;
       fence_after_sync();
-      const uint64_t vd = sw128_mn_desc(tile_at(vp) + h * 8192, 16384);
+      const uint64_t vd = sw128_mn_desc(tile_at(slot) + h * 8192, 16384);
 #pragma unroll
       for (int k = 0; k < KT / 32; ++k)
-        mma_ts(leader, tmem + O_COL + HD * s, tmem + 128 * s + 64 * h + 8 * k,
-               desc_add(vd, k * 2048), ID_O, !first || k > 0);
-      commit(leader, &ctl.o_full[s]);
-    };
-    auto value_tile = [&](int t, const RingPos &vp) {
-      if (!wait(&ctl.kv_full[vp.slot], vp.phase)) return;
-      if (hidden_from<MODE>(u, t) < KT) {
-        wait(&ctl.v_ok[vp.slot], ph_v >> vp.slot);
-        ph_v ^= 1u << vp.slot;
-      }
+        mma_ts(leader, o_tm, s_tm + 64 * h + 8 * k, desc_add(vd, k * 2048), ID_O, !first || k > 0);
+      commit(leader, &ctl.o_full[st]);
+      if (last) commit(leader, &ctl.o_last[st]);
+      return true;
     };
     // Two S per stream: the next half's scores are under way while the softmax works on this
     // half's. S(i + 2) goes where P(i) was, behind P(i) V(i) in the same pipe.
     while (ok && walk.next(a, u)) {
       const int n = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0);
-      const int n0 = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, 0), 0);
-      const int n1 = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, 1), 0);
-#define N_S(s) ((s) ? n1 : n0)
-#pragma unroll
-      for (int s = 0; s < (MODE == MODE_KEYS ? 1 : 2); ++s)
-        if (ok && N_S(s) > 0) {
-          wait(&ctl.q_full[s], ph_q[s]);
-          ph_q[s] ^= 1;
+      const int n_mine = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, st), 0);
+      if (MODE == MODE_KEYS || n_mine > 0) {
+        ok = warp_wait(&ctl.q_full[MODE == MODE_KEYS ? 0 : st], ph_q, abort);
+        ph_q ^= 1;
+        fence_after_sync();
+      }
+      for (int i = 0; ok && i < C::AHEAD && i < n; ++i) {
+        ok = warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
+        if (!ok) break;
+        if (MODE != MODE_KEYS || i == st) {
+          if (n_mine > 0) scores(0, pos.slot);
+          if (n_mine > 1) scores(1, pos.slot);
         }
-      fence_after_sync();
-      if constexpr (MODE == MODE_KEYS) {
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (s >= n || !ok) break;
-          if (!wait(&ctl.kv_full[pos.slot], pos.phase)) break;
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-            if (h < N_S(s)) scores(s, h, pos);
-          commit(leader, &ctl.kv_empty[pos.slot]);
-          pos.next(C::SLOTS);
-        }
-        for (int i = 0; i < n && ok; i += 2) {
-          RingPos vp[2], kp[2];
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            vp[s] = kp[s] = pos;
-            if (i + s >= n) continue;
-            pos.next(C::SLOTS);
-            kp[s] = pos;
-            if (i + s + 2 < n) pos.next(C::SLOTS);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (!ok || i + s >= n) break;
-              if (i + h < N_S(s)) {
-                if (h == 0) value_tile(u.t0 + i + s, vp[s]);
-                if (ok) values(s, h, vp[s], i + h == 0);
-                if (ok && i + h + 2 < N_S(s)) {
-                  if (h == 0) wait(&ctl.kv_full[kp[s].slot], kp[s].phase);
-                  if (ok) scores(s, h, kp[s]);
-                }
-              }
-              if (!ok || h == 0) continue;
-              commit(leader, &ctl.kv_empty[vp[s].slot]);
-              if (i + s + 2 < n) commit(leader, &ctl.kv_empty[kp[s].slot]);
-            }
-        }
-      } else {
-        if (ok) wait(&ctl.kv_full[pos.slot], pos.phase);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int s = 0; s < 2; ++s)
-            if (ok && h < N_S(s)) scores(s, h, pos);
         commit(leader, &ctl.kv_empty[pos.slot]);
         pos.next(C::SLOTS);
-        for (int i = 0; i < n && ok; ++i) {
-          const RingPos vp = pos;
-          pos.next(C::SLOTS);
-          const RingPos kp = pos;
-          const bool more = i + 1 < n;
-          if (more) pos.next(C::SLOTS);
-          value_tile(u.t0 + i, vp);
-          if (ok && more) wait(&ctl.kv_full[kp.slot], kp.phase);
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (!ok || 2 * i + h >= N_S(s)) continue;
-              values(s, h, vp, 2 * i + h == 0);
-              if (ok && 2 * i + h + 2 < N_S(s)) scores(s, h, kp);
-            }
-          if (!ok) break;
-          commit(leader, &ctl.kv_empty[vp.slot]);
-          if (more) commit(leader, &ctl.kv_empty[kp.slot]);
-        }
       }
-#undef N_S
+      for (int i = 0; ok && i < n; ++i) {
+        const int v_slot = pos.slot;
+        ok = warp_wait(&ctl.kv_full[v_slot], pos.phase, abort);
+        pos.next(C::SLOTS);
+        if (ok && hidden_from<MODE>(u, u.t0 + i) < KT) {
+          ok = warp_wait(&ctl.v_ok[v_slot], ph_v >> v_slot & 1, abort);
+          ph_v ^= 1u << v_slot;
+        }
+        const bool more = i + C::AHEAD < n;
+        const int k_slot = pos.slot;
+        if (ok && more) {
+          ok = warp_wait(&ctl.kv_full[k_slot], pos.phase, abort);
+          pos.next(C::SLOTS);
+        }
+        if (!ok) break;
+        if (MODE != MODE_KEYS || (i & 1) == st) {
+          const int b = MODE == MODE_KEYS ? i - st : 2 * i;  // the stream's first half of the tile
+          if (b < n_mine) {
+            ok = values(0, v_slot, b == 0, b + 1 == n_mine);
+            if (ok && b + 2 < n_mine) scores(0, k_slot);
+          }
+          if (ok && b + 1 < n_mine) {
+            ok = values(1, v_slot, false, b + 2 == n_mine);
+            if (ok && b + 3 < n_mine) scores(1, k_slot);
+          }
+          if (!ok) break;
+        }
+        commit(leader, &ctl.kv_empty[v_slot]);
+        if (more) commit(leader, &ctl.kv_empty[k_slot]);
+      }
     }
     // Every MMA and commit has completed before the CTA gives its tensor memory back.
     commit(leader, &ctl.drain);
@@ -799,8 +762,7 @@ __global__ void __launch_bounds__(384, 1)
           }
           // A row is 8 16-byte pieces of each 64-column slab, whatever their swizzled order.
           char *tile = base + (C::NQ + pos.slot) * C::TILE;
-          const int half = warp - 10, pieces = (r1 - r0) * 8;
-          const int p0 = r0 * 8 + half * pieces / 2, p1 = r0 * 8 + (half + 1) * pieces / 2;
+          const int p0 = r0 * 8, p1 = r1 * 8;
           uint32_t top = 0;
           for (int s = 0; s < C::SLABS; ++s)
 #pragma unroll 4
