@@ -320,12 +320,16 @@ def decode_attention(k_hist, v_hist, k_exact, k_exact_pos, v_exact, v_exact_pos,
 # Dense attention around the compressed cache: the rotary embedding, the prompt's exact attention
 # (where Algorithm 1 starts) and drafted tokens over a reconstructed cache (Algorithm 3 step 9).
 
+# (torch.cuda.current_stream() builds a stream object, 3 us of a short call's time.)
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 class _On:
     """The device and stream of a call: ``with _On(device, stream) as s`` makes the device current
-    and, for a given stream, allocates on it."""
+    and allocates on the stream; ``s`` is its raw handle."""
 
     def __init__(self, device, stream):
-        self.ctx = None
+        self.device, self.ctx = device, None
         if stream is not None:
             if stream.device != device:
                 raise ValueError("the stream belongs to another device than the tensors")
@@ -336,7 +340,7 @@ class _On:
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(self.device.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
@@ -347,23 +351,19 @@ def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> IskvHeads:
     """``t`` ([batch,] row, head, head_dim) as an ``iskv_heads``; its last axis is contiguous."""
     if t.device != device or not t.is_cuda:
         raise ValueError(f"{name}: all tensors must live on one CUDA device")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {shape}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
     st = t.stride()
     if st[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}: the last axis must be contiguous")
-    # The stride of an axis of length one is never used; torch leaves it arbitrary.
-    lead = [s if n > 1 else 0 for s, n in zip(st[:-1], shape[:-1])]
-    if len(lead) == 2:
-        lead.insert(0, 0)
-    return IskvHeads(t.data_ptr(), *lead)
+    return IskvHeads(t.data_ptr(), 0 if len(st) == 3 else st[0], st[-3], st[-2])
 
 
 def _ints(t: torch.Tensor, name: str, shape, device) -> int:
-    if t.device != device or t.dtype != torch.int32 or not t.is_contiguous() \
-            or tuple(t.shape) != shape:
+    if t.device != device or t.dtype is not torch.int32 or not t.is_contiguous() \
+            or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
     return t.data_ptr()
 
@@ -379,7 +379,12 @@ def _status_word(t, device):
 def _rank(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} axes, expected {n}")
-    return tuple(t.shape)
+    return t.shape
+
+
+def _new(t: torch.Tensor) -> torch.Tensor:
+    """A contiguous tensor of ``t``'s shape and dtype."""
+    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None, stream=None):
@@ -394,7 +399,7 @@ def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None,
     pp = _ints(pos, "pos", (n,), dev)
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=x.dtype, device=dev)
+            out = _new(x)
         ho = _heads(out, "out", shape, x.dtype, dev)
         _lib.check(_lib.load().iskv_rope(hx, pp, n, heads, hd, theta, inverse, dt, ho, s), "rope")
     return out
@@ -421,7 +426,7 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
             seqs = max(cu_seqlens.numel() - 1, 0)
             cp = _ints(cu_seqlens, "cu_seqlens", (seqs + 1,), dev)
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
+            out = _new(q)
         ho = _heads(out, "out", shape, dtype, dev)
         _lib.check(_lib.load().iskv_prompt_attention(
             hq, hk, hv, cp, seqs, rows, nq, nkv, hd,
@@ -459,7 +464,7 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     lib = _lib.load()
     with _On(dev, stream) as s:
         if out is None:
-            out = torch.empty(shape, dtype=dtype, device=dev)
+            out = _new(q)
         ho = _heads(out, "out", shape, dtype, dev)
         if ws is None:
             # A buffer of this call's own, from the stream's pool: calls on several streams and

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "iskv.h"
 
 namespace iskv {
@@ -56,6 +58,21 @@ bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e);
 // Joins the partial results of a tree call whose kernel ran `grid` CTAs over units of `rows` rows
 // and tiles of `keys` keys.
 cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, cudaStream_t s);
+
+// A kernel's dynamic shared-memory limit, raised once per device (the first 64 of a process).
+struct SmemLimit {
+  std::atomic<uint64_t> done{0};
+  cudaError_t raise(const void *kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 struct RopeArgs {
   const void *x;

@@ -33,6 +33,15 @@ iskv_status check_heads(const iskv_heads *x, const char *name, int32_t dtype, bo
   return ISKV_OK;
 }
 
+// The stride of an axis of length one is never used; callers may leave anything there.
+iskv_heads walked(const iskv_heads *x, int64_t entries, int64_t rows, int64_t heads) {
+  iskv_heads y = *x;
+  if (entries <= 1) y.batch = 0;
+  if (rows <= 1) y.row = 0;
+  if (heads <= 1) y.head = 0;
+  return y;
+}
+
 iskv_status check_shape(int32_t n_q, int32_t n_kv, int32_t head_dim, float scale, const char *who) {
   if (n_kv < 1 || n_kv > 1024 || n_q < 1 || n_q % n_kv || n_q / n_kv > 64)
     return fail(ISKV_ERR_SHAPE, "%s: need n_q_heads a multiple of n_kv_heads (1..1024), at most 64 "
@@ -82,13 +91,14 @@ iskv_status iskv_rope(const iskv_heads *x, const int32_t *pos, int64_t n, int32_
     return fail(ISKV_ERR_ARG, "%s: in place needs equal strides", who);
   if ((n > 1 && out->row == 0) || (n_heads > 1 && out->head == 0))
     return fail(ISKV_ERR_SHAPE, "%s: out has a stride of 0", who);
+  const iskv_heads xs = walked(x, 1, n, n_heads), os = walked(out, 1, n, n_heads);
   RopeArgs a;
-  a.x = x->data;
-  a.out = out->data;
-  a.x_row = x->row;
-  a.x_head = x->head;
-  a.o_row = out->row;
-  a.o_head = out->head;
+  a.x = xs.data;
+  a.out = os.data;
+  a.x_row = xs.row;
+  a.x_head = xs.head;
+  a.o_row = os.row;
+  a.o_head = os.head;
   a.pos = pos;
   a.n = n;
   a.heads = n_heads;
@@ -131,10 +141,10 @@ iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, cons
   if ((n_rows > 1 && out->row == 0) || (n_q_heads > 1 && out->head == 0))
     return fail(ISKV_ERR_SHAPE, "%s: out has a stride of 0", who);
   DenseArgs a = {};
-  a.q = *q;
-  a.k = *k;
-  a.v = *v;
-  a.out = *out;
+  a.q = walked(q, 1, n_rows, n_q_heads);
+  a.k = walked(k, 1, n_rows, n_kv_heads);
+  a.v = walked(v, 1, n_rows, n_kv_heads);
+  a.out = walked(out, 1, n_rows, n_q_heads);
   a.cu = cu_seqlens;
   a.batch = n_seqs;
   a.rows = n_rows;
@@ -211,12 +221,12 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   if (ws_bytes < need)
     return fail(ISKV_ERR_WORKSPACE, "%s: workspace too small (%zu < %zu bytes)", who, ws_bytes, need);
   DenseArgs a = {};
-  a.q = *q;
-  a.k = *k_draft;
-  a.v = *v_draft;
-  a.kc = *k_cache;
-  a.vc = *v_cache;
-  a.out = *out;
+  a.q = walked(q, batch, n_nodes, n_q_heads);
+  a.k = walked(k_draft, batch, n_nodes, n_kv_heads);
+  a.v = walked(v_draft, batch, n_nodes, n_kv_heads);
+  a.kc = walked(k_cache, batch, n_cap, n_kv_heads);
+  a.vc = walked(v_cache, batch, n_cap, n_kv_heads);
+  a.out = walked(out, batch, n_nodes, n_q_heads);
   a.n_cached = n_cached;
   a.parents = parents;
   a.tree = 1;

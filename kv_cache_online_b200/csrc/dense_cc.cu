@@ -297,14 +297,17 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
   }
 }
 
-// A block: 32 rows (lanes) and four columns of one unit; its four warps take every fourth part of the
-// unit, with a running maximum each, and add up in shared memory with weights 2^(m_i - max m).
-// Latency bound (a few KB per block): the loads of four parts are in flight together.
+// A block: 32 rows (lanes) and up to JOIN_COLS groups of four columns of one unit; its four warps take
+// every fourth part of the unit, with a running maximum each, and add up in shared memory with
+// weights 2^(m_i - max m). Latency bound (a few KB per block): the loads of four parts are in
+// flight together; the launch gives a block more column groups once there are blocks enough.
+constexpr int JOIN_COLS = 8;
+
 template <typename T, int ROWS, int KT>
 __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
-                                                    int hd_pad) {
+                                                    int hd_pad, int cols_per) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[4][6][32];
+  __shared__ float part[4][2 + 4 * JOIN_COLS][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   TreeLine<ROWS, KT> line;
   line.begin(a, grid, 0);
@@ -319,82 +322,107 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int c0 = u0 / line.per, c1 = (u0 + n - 1) / line.per;
   if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
   const int n_rows = min(ROWS, rows_all - blk * ROWS);
-  const int cols = (a.head_dim + 3) / 4, c4 = blockIdx.y % cols;
-  const int r = blockIdx.y / cols * 32 + lane;
+  const int groups = (a.head_dim + 4 * cols_per - 1) / (4 * cols_per);
+  const int g0 = blockIdx.y % groups * cols_per, gn = min(cols_per, (a.head_dim + 3) / 4 - g0);
+  const int r = blockIdx.y / groups * 32 + lane;
   if (r - lane >= n_rows) return;
-  const int pr = blk * ROWS + min(r, n_rows - 1), node = pr / a.group;
+  const int rr = min(r, n_rows - 1);
   const size_t slot_floats = dense_slot_floats(ROWS, hd_pad);
   // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's share:
   // slot 0.
-  const float *ws = static_cast<const float *>(a.ws) + (min(r, n_rows - 1));
-  const int first_slot = 2 * c0 + 1;
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  auto slot = [&](int c) {
+    return static_cast<const float *>(a.ws) + (c == c0 ? 2 * c + 1 : 2 * c) * slot_floats;
+  };
+  float m = -INFINITY, l = 0.f;
+  float4 o[JOIN_COLS];
+#pragma unroll
+  for (int g = 0; g < JOIN_COLS; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = c0 + warp; c <= c1; c += 16) {
-    float mi[4], li[4];
-    float4 v[4];
+    float w[4], li[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      mi[i] = -INFINITY;
-      li[i] = 0.f;
-      v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (c + 4 * i <= c1) {
-        const float *w = ws + (c + 4 * i == c0 ? first_slot : 2 * (c + 4 * i)) * slot_floats;
-        mi[i] = w[(size_t)ROWS * hd_pad];
-        li[i] = w[(size_t)ROWS * (hd_pad + 1)];
-        v[i] = *reinterpret_cast<const float4 *>(
-            static_cast<const float *>(a.ws) +
-            (c + 4 * i == c0 ? first_slot : 2 * (c + 4 * i)) * slot_floats +
-            ((size_t)c4 * ROWS + min(r, n_rows - 1)) * 4);
-      }
+      const bool in = c + 4 * i <= c1;
+      const float *s = slot(min(c + 4 * i, c1));
+      w[i] = in ? s[(size_t)ROWS * hd_pad + rr] : -INFINITY;
+      li[i] = in ? s[(size_t)ROWS * (hd_pad + 1) + rr] : 0.f;
+    }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) mn = fmaxf(mn, w[i]);
+    const float ref = mn == -INFINITY ? 0.f : mn, f = ex2(m - ref);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // A part that saw nothing has m = -inf and l = 0 (its O may be anything); with m = -inf and
+      // another l, not-a-number scores alone were seen.
+      w[i] = w[i] == -INFINITY && li[i] == 0.f ? -1.f : ex2(w[i] - ref);
+      if (!(w[i] < 0.f)) l = fmaf(li[i], w[i], l);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (mi[i] == -INFINITY && li[i] == 0.f) continue;  // a part that saw nothing
-      const float mn = fmaxf(m, mi[i]), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = ex2(m - ref), g = ex2(mi[i] - ref);
-      m = mn;
-      l = l * f + li[i] * g;
-      o[0] = o[0] * f + v[i].x * g;
-      o[1] = o[1] * f + v[i].y * g;
-      o[2] = o[2] * f + v[i].z * g;
-      o[3] = o[3] * f + v[i].w * g;
+    for (int g = 0; g < JOIN_COLS; ++g) {
+      if (g >= gn) break;
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        v[i] = reinterpret_cast<const float4 *>(slot(min(c + 4 * i, c1)))[(g0 + g) * ROWS + rr];
+      o[g].x *= f;
+      o[g].y *= f;
+      o[g].z *= f;
+      o[g].w *= f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (w[i] < 0.f) continue;
+        o[g].x = fmaf(v[i].x, w[i], o[g].x);
+        o[g].y = fmaf(v[i].y, w[i], o[g].y);
+        o[g].z = fmaf(v[i].z, w[i], o[g].z);
+        o[g].w = fmaf(v[i].w, w[i], o[g].w);
+      }
     }
   }
   part[warp][0][lane] = m;
   part[warp][1][lane] = l;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) part[warp][2 + e][lane] = o[e];
+  for (int g = 0; g < JOIN_COLS; ++g) {
+    if (g >= gn) break;
+    part[warp][2 + 4 * g][lane] = o[g].x;
+    part[warp][3 + 4 * g][lane] = o[g].y;
+    part[warp][4 + 4 * g][lane] = o[g].z;
+    part[warp][5 + 4 * g][lane] = o[g].w;
+  }
   __syncthreads();
-  if (warp) return;
-  float top = m;
+  if (r >= n_rows) return;
+  float top = -INFINITY, f[4];
 #pragma unroll
-  for (int w = 1; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
   const float ref = top == -INFINITY ? 0.f : top;
   l = 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) o[e] = 0.f;
-#pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const float f = ex2(part[w][0][lane] - ref);
-    l += part[w][1][lane] * f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] += part[w][2 + e][lane] * f;
+    f[w] = ex2(part[w][0][lane] - ref);
+    l += part[w][1][lane] * f[w];
   }
-  if (r >= n_rows) return;
-  const bool live = l != 0.f;  // padding nodes came as parts that saw nothing
-  const float inv = 1.f / l;
+  const float inv = l != 0.f ? 1.f / l : 0.f;  // padding nodes came as parts that saw nothing
+  const int pr = blk * ROWS + r, node = pr / a.group;
   T *out = static_cast<T *>(a.out.data) +
            at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);
+  for (int g = warp; g < gn; g += 4)
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (c4 * 4 + e < a.head_dim) out[c4 * 4 + e] = from_f<T>(live ? o[e] * inv : 0.f);
+    for (int e = 0; e < 4; ++e) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) x += part[w][2 + 4 * g + e][lane] * f[w];
+      const int col = (g0 + g) * 4 + e;
+      if (col < a.head_dim) out[col] = from_f<T>(l != 0.f ? x * inv : 0.f);
+    }
 }
 
 template <typename T, int HD, bool TREE, bool VEC>
 cudaError_t run(const DenseArgs &a, int grid, cudaStream_t s) {
   auto *kernel = k_dense_cc<T, HD, TREE, VEC>;
   const int smem = (int)sizeof(Smem<HD>);
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void *>(kernel), smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, NT, smem, s>>>(a);
   count_launches(1);
@@ -411,8 +439,12 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(a.batch * a.n_kv * blocks),
-                     (unsigned)(chunks * ((a.head_dim + 3) / 4)));
+  // One group of four columns per block until the blocks fill the SMs (148 x 16), then more.
+  const int cols = (a.head_dim + 3) / 4;
+  const int64_t units = (int64_t)a.batch * a.n_kv * blocks;
+  int64_t per = units * chunks * cols / (148 * 16);
+  per = per < 1 ? 1 : per > JOIN_COLS ? JOIN_COLS : per;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)(chunks * ((cols + per - 1) / per)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = &attr;
@@ -421,9 +453,9 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
   cudaError_t e = cudaErrorInvalidValue;
   with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (keys == 64) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64>, a, grid, pad);
-    else if (rows == 128) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128>, a, grid, pad);
-    else e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128>, a, grid, pad);
+    if (keys == 64) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64>, a, grid, pad, (int)per);
+    else if (rows == 128) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128>, a, grid, pad, (int)per);
+    else e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128>, a, grid, pad, (int)per);
   });
   count_launches(1);
   return e;

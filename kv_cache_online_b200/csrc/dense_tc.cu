@@ -864,7 +864,8 @@ cudaError_t run(const DenseArgs &a, const Maps &maps, int grid, cudaStream_t s) 
   auto *kernel = k_dense_tc<T, HD, MODE>;
   constexpr int smem = Cfg<HD, MODE>::SMEM;
   static_assert(smem <= 232448 && Cfg<HD, MODE>::SLOTS >= 4, "ring does not fit");
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static SmemLimit limit;
+  cudaError_t e = limit.raise(reinterpret_cast<const void *>(kernel), smem);
   if (e != cudaSuccess) return e;
   kernel<<<grid, 384, smem, s>>>(a, maps);
   count_launches(1);
