@@ -158,7 +158,11 @@ struct TreeLine {
     if (x >= end) return false;
     const int lane = threadIdx.x & 31;
     int before = 0;
-    for (int b0 = 0;; b0 += 32) {
+    if (a.batch == 1) {
+      u.b = 0;
+      u.len = __shfl_sync(0xffffffffu, len0, 0);
+    }
+    for (int b0 = 0; a.batch > 1; b0 += 32) {
       const int n = entry_tiles(a, b0 + lane);
       int sum = n;
 #pragma unroll

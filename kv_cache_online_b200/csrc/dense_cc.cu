@@ -306,8 +306,7 @@ constexpr int JOIN_COLS = 8;
 template <typename T, int ROWS, int KT>
 __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
                                                     int hd_pad, int cols_per) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[4][2 + 4 * JOIN_COLS][32];
+  __shared__ float part[4][2 + 4 * JOIN_COLS][33], factor[5][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   TreeLine<ROWS, KT> line;
   line.begin(a, grid, 0);
@@ -333,19 +332,28 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   auto slot = [&](int c) {
     return static_cast<const float *>(a.ws) + (c == c0 ? 2 * c + 1 : 2 * c) * slot_floats;
   };
+  // Up to here only the call's inputs were read; the parts need the kernel before this one.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   float m = -INFINITY, l = 0.f;
   float4 o[JOIN_COLS];
 #pragma unroll
   for (int g = 0; g < JOIN_COLS; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = c0 + warp; c <= c1; c += 16) {
     float w[4], li[4];
+    float4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const bool in = c + 4 * i <= c1;
       const float *s = slot(min(c + 4 * i, c1));
-      w[i] = in ? s[(size_t)ROWS * hd_pad + rr] : -INFINITY;
-      li[i] = in ? s[(size_t)ROWS * (hd_pad + 1) + rr] : 0.f;
+      w[i] = s[(size_t)ROWS * hd_pad + rr];
+      li[i] = s[(size_t)ROWS * (hd_pad + 1) + rr];
+      v[i] = reinterpret_cast<const float4 *>(s)[g0 * ROWS + rr];
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + 4 * i > c1) {
+        w[i] = -INFINITY;
+        li[i] = 0.f;
+      }
     float mn = m;
 #pragma unroll
     for (int i = 0; i < 4; ++i) mn = fmaxf(mn, w[i]);
@@ -362,10 +370,11 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
 #pragma unroll
     for (int g = 0; g < JOIN_COLS; ++g) {
       if (g >= gn) break;
-      float4 v[4];
+      if (g > 0) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        v[i] = reinterpret_cast<const float4 *>(slot(min(c + 4 * i, c1)))[(g0 + g) * ROWS + rr];
+        for (int i = 0; i < 4; ++i)
+          v[i] = reinterpret_cast<const float4 *>(slot(min(c + 4 * i, c1)))[(g0 + g) * ROWS + rr];
+      }
       o[g].x *= f;
       o[g].y *= f;
       o[g].z *= f;
@@ -391,30 +400,34 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
     part[warp][5 + 4 * g][lane] = o[g].w;
   }
   __syncthreads();
-  if (r >= n_rows) return;
-  float top = -INFINITY, f[4];
+  if (warp == 0) {
+    float top = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
-  const float ref = top == -INFINITY ? 0.f : top;
-  l = 0.f;
+    for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
+    const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    f[w] = ex2(part[w][0][lane] - ref);
-    l += part[w][1][lane] * f[w];
-  }
-  const float inv = l != 0.f ? 1.f / l : 0.f;  // padding nodes came as parts that saw nothing
-  const int pr = blk * ROWS + r, node = pr / a.group;
-  T *out = static_cast<T *>(a.out.data) +
-           at(a.out, b, node, (int64_t)kvh * a.group + pr % a.group);
-  for (int g = warp; g < gn; g += 4)
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float x = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) x += part[w][2 + 4 * g + e][lane] * f[w];
-      const int col = (g0 + g) * 4 + e;
-      if (col < a.head_dim) out[col] = from_f<T>(l != 0.f ? x * inv : 0.f);
+    for (int w = 0; w < 4; ++w) {
+      const float f = ex2(part[w][0][lane] - ref);
+      factor[w][lane] = f;
+      sum += part[w][1][lane] * f;
     }
+    factor[4][lane] = sum;
+  }
+  __syncthreads();
+  // Rows leave with neighbouring columns in neighbouring lanes.
+  const int width = 4 * gn, row0 = blk * ROWS + r - lane, rows = min(32, n_rows - (r - lane));
+  for (int i = threadIdx.x; i < rows * width; i += 128) {
+    const int row = i / width, x = i - row * width, col = g0 * 4 + x;
+    if (col >= a.head_dim) continue;
+    const float sum = factor[4][row];
+    float v = 0.f;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v += part[w][2 + x][row] * factor[w][row];
+    const int pr = row0 + row, node = pr / a.group;
+    // padding nodes came as parts that saw nothing
+    static_cast<T *>(a.out.data)[at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) +
+                                 col] = from_f<T>(sum != 0.f ? v / sum : 0.f);
+  }
 }
 
 template <typename T, int HD, bool TREE, bool VEC>

@@ -327,9 +327,9 @@ __global__ void __launch_bounds__(384, 1)
   Unit u;
   walk.begin(a);
 
-  // Registers: 256 x 208 + 128 x 88 = 64,512, the launch's 384 x 168.
+  // Registers: 256 x 192 + 128 x 120 = 64,512, the launch's 384 x 168.
   if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     // ------------------------------------------------------------------------- softmax
     const int st = warp / 4, quad = warp & 3;     // stream; 32 rows
     const int row = quad * 32 + lane;             // row of the stream's tile
@@ -506,8 +506,8 @@ __global__ void __launch_bounds__(384, 1)
       const bool fix = *(volatile int *)&ctl.fix[walk.count & 7] == walk.count;
       const bool whole = !TREE || (u.t0 == 0 && u.t1 == u.n_tiles);
       const bool mine = row < tile_rows;
-      const bool live = !TREE || (mask[0] | mask[1] | mask[2] | mask[3]);
       if (busy) {
+        const bool live = !TREE || (mask[0] | mask[1] | mask[2] | mask[3]);
         const uint32_t o0 = tmem + lanes + O_COL;
         const float inv = 1.f / l;
         const bool zero = l == 0.f || !live;
@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
   if (warp == 8) {
     // ------------------------------------------------------------------------- loads
     RingPos pos;
