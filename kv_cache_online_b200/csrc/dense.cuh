@@ -5,8 +5,8 @@
 // key and value and a single token still fills `group` rows.
 //
 // Prompt: a unit is (sequence, key/value head, block of ROWS packed rows) and runs over the keys
-// up to its last token. CTAs take units in descending row-block index over all sequences (the
-// longest runs first: the block scheduler then packs the short ones behind them).
+// up to its last token. CTAs take units in descending row-block index over all sequences: the longest
+// runs first, the short ones fill up behind them.
 //
 // Tree: a unit is (batch entry, key/value head, row block); its keys are the cached rows, in tiles
 // of KT, followed by the drafted nodes in tiles of KT. All units' tiles form one line that is cut

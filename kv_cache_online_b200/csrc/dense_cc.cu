@@ -297,15 +297,16 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
   }
 }
 
-// A block: 32 rows (lanes) and up to JOIN_COLS groups of four columns of one unit; its four warps take
-// every fourth part of the unit, with a running maximum each, and add up in shared memory with
-// weights 2^(m_i - max m). Latency bound (a few KB per block): the loads of four parts are in
-// flight together; the launch gives a block more column groups once there are blocks enough.
+// A block: 32 rows (lanes) of one unit. SPLIT: its four warps take every fourth part of the unit for
+// the same `per` groups of four columns, with a running maximum each, and add up in shared memory
+// with weights 2^(m_i - max m) (few units of many parts each); otherwise every warp takes all parts
+// for `per` column groups of its own (many units, a few parts each). Latency bound, a few KB per
+// warp: the loads of four parts are in flight together.
 constexpr int JOIN_COLS = 8;
 
-template <typename T, int ROWS, int KT>
+template <typename T, int ROWS, int KT, bool SPLIT>
 __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
-                                                    int hd_pad, int cols_per) {
+                                                    int hd_pad, int per) {
   __shared__ float part[4][2 + 4 * JOIN_COLS][33], factor[5][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   TreeLine<ROWS, KT> line;
@@ -321,11 +322,13 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int c0 = u0 / line.per, c1 = (u0 + n - 1) / line.per;
   if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
   const int n_rows = min(ROWS, rows_all - blk * ROWS);
-  const int groups = (a.head_dim + 4 * cols_per - 1) / (4 * cols_per);
-  const int g0 = blockIdx.y % groups * cols_per, gn = min(cols_per, (a.head_dim + 3) / 4 - g0);
+  const int block_cols = SPLIT ? per : 4 * per, all_cols = (a.head_dim + 3) / 4;
+  const int groups = (all_cols + block_cols - 1) / block_cols;
   const int r = blockIdx.y / groups * 32 + lane;
   if (r - lane >= n_rows) return;
   const int rr = min(r, n_rows - 1);
+  const int g0 = blockIdx.y % groups * block_cols + (SPLIT ? 0 : warp * per);
+  const int gn = max(0, min(per, all_cols - g0));  // this warp's column groups
   const size_t slot_floats = dense_slot_floats(ROWS, hd_pad);
   // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's share:
   // slot 0.
@@ -334,23 +337,24 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   };
   // Up to here only the call's inputs were read; the parts need the kernel before this one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int STEP = SPLIT ? 4 : 1;
   float m = -INFINITY, l = 0.f;
   float4 o[JOIN_COLS];
 #pragma unroll
   for (int g = 0; g < JOIN_COLS; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int c = c0 + warp; c <= c1; c += 16) {
+  for (int c = c0 + (SPLIT ? warp : 0); c <= c1; c += 4 * STEP) {
     float w[4], li[4];
     float4 v[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float *s = slot(min(c + 4 * i, c1));
+      const float *s = slot(min(c + STEP * i, c1));
       w[i] = s[(size_t)ROWS * hd_pad + rr];
       li[i] = s[(size_t)ROWS * (hd_pad + 1) + rr];
-      v[i] = reinterpret_cast<const float4 *>(s)[g0 * ROWS + rr];
+      v[i] = reinterpret_cast<const float4 *>(s)[min(g0, all_cols - 1) * ROWS + rr];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (c + 4 * i > c1) {
+      if (c + STEP * i > c1) {
         w[i] = -INFINITY;
         li[i] = 0.f;
       }
@@ -373,7 +377,7 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
       if (g > 0) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          v[i] = reinterpret_cast<const float4 *>(slot(min(c + 4 * i, c1)))[(g0 + g) * ROWS + rr];
+          v[i] = reinterpret_cast<const float4 *>(slot(min(c + STEP * i, c1)))[(g0 + g) * ROWS + rr];
       }
       o[g].x *= f;
       o[g].y *= f;
@@ -389,44 +393,58 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
       }
     }
   }
-  part[warp][0][lane] = m;
-  part[warp][1][lane] = l;
+  // Rows leave through shared memory with neighbouring columns in neighbouring lanes. l = 0: padding
+  // nodes, which came as parts that saw nothing.
+  const int row0 = blk * ROWS + r - lane, rows = min(32, n_rows - (r - lane)), width = 4 * gn;
+  auto put = [&](int row, int x, float v) {
+    const int col = g0 * 4 + x;
+    if (col >= a.head_dim) return;
+    const int pr = row0 + row, node = pr / a.group;
+    static_cast<T *>(a.out.data)[at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) +
+                                 col] = from_f<T>(v);
+  };
+  const float scale = SPLIT ? 1.f : l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
   for (int g = 0; g < JOIN_COLS; ++g) {
     if (g >= gn) break;
-    part[warp][2 + 4 * g][lane] = o[g].x;
-    part[warp][3 + 4 * g][lane] = o[g].y;
-    part[warp][4 + 4 * g][lane] = o[g].z;
-    part[warp][5 + 4 * g][lane] = o[g].w;
+    const bool keep = SPLIT || l != 0.f;
+    part[warp][2 + 4 * g][lane] = keep ? o[g].x * scale : 0.f;
+    part[warp][3 + 4 * g][lane] = keep ? o[g].y * scale : 0.f;
+    part[warp][4 + 4 * g][lane] = keep ? o[g].z * scale : 0.f;
+    part[warp][5 + 4 * g][lane] = keep ? o[g].w * scale : 0.f;
   }
-  __syncthreads();
-  if (warp == 0) {
-    float top = -INFINITY, sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      const float f = ex2(part[w][0][lane] - ref);
-      factor[w][lane] = f;
-      sum += part[w][1][lane] * f;
+  if constexpr (!SPLIT) {
+    __syncwarp();
+    for (int i = lane; i < rows * width; i += 32) {
+      const int row = i / width, x = i - row * width;
+      put(row, x, part[warp][2 + x][row]);
     }
-    factor[4][lane] = sum;
-  }
-  __syncthreads();
-  // Rows leave with neighbouring columns in neighbouring lanes.
-  const int width = 4 * gn, row0 = blk * ROWS + r - lane, rows = min(32, n_rows - (r - lane));
-  for (int i = threadIdx.x; i < rows * width; i += 128) {
-    const int row = i / width, x = i - row * width, col = g0 * 4 + x;
-    if (col >= a.head_dim) continue;
-    const float sum = factor[4][row];
-    float v = 0.f;
+  } else {
+    part[warp][0][lane] = m;
+    part[warp][1][lane] = l;
+    __syncthreads();
+    if (warp == 0) {
+      float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) v += part[w][2 + x][row] * factor[w][row];
-    const int pr = row0 + row, node = pr / a.group;
-    // padding nodes came as parts that saw nothing
-    static_cast<T *>(a.out.data)[at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) +
-                                 col] = from_f<T>(sum != 0.f ? v / sum : 0.f);
+      for (int w = 0; w < 4; ++w) top = fmaxf(top, part[w][0][lane]);
+      const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = ex2(part[w][0][lane] - ref);
+        factor[w][lane] = f;
+        sum += part[w][1][lane] * f;
+      }
+      factor[4][lane] = sum;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * width; i += 128) {
+      const int row = i / width, x = i - row * width;
+      const float sum = factor[4][row];
+      float v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) v += part[w][2 + x][row] * factor[w][row];
+      put(row, x, sum != 0.f ? v / sum : 0.f);
+    }
   }
 }
 
@@ -452,12 +470,15 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  // One group of four columns per block until the blocks fill the SMs (148 x 16), then more.
   const int cols = (a.head_dim + 3) / 4;
   const int64_t units = (int64_t)a.batch * a.n_kv * blocks;
-  int64_t per = units * chunks * cols / (148 * 16);
-  per = per < 1 ? 1 : per > JOIN_COLS ? JOIN_COLS : per;
-  cfg.gridDim = dim3((unsigned)units, (unsigned)(chunks * ((cols + per - 1) / per)));
+  // `grid` shares over `units` units: with fewer than about 40 units (four parts or more each) the
+  // parts of a unit are split over warps, one column group per block; otherwise whole rows per
+  // block (64 units of 192 rows and three to four parts: 24 us split, 9 us not).
+  const bool split = units * 4 <= grid;
+  const int per = split ? 1 : (cols + 3) / 4 > JOIN_COLS ? JOIN_COLS : (cols + 3) / 4;
+  const int block_cols = split ? per : 4 * per;
+  cfg.gridDim = dim3((unsigned)units, (unsigned)(chunks * ((cols + block_cols - 1) / block_cols)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
   cfg.attrs = &attr;
@@ -466,9 +487,14 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
   cudaError_t e = cudaErrorInvalidValue;
   with_dtype(a.dtype, [&](auto tag) {
     using T = decltype(tag);
-    if (keys == 64) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64>, a, grid, pad, (int)per);
-    else if (rows == 128) e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128>, a, grid, pad, (int)per);
-    else e = cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128>, a, grid, pad, (int)per);
+    auto go = [&](auto sp) {
+      constexpr bool S = decltype(sp)::value;
+      e = keys == 64    ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64, S>, a, grid, pad, per)
+          : rows == 128 ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128, S>, a, grid, pad, per)
+                        : cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128, S>, a, grid, pad, per);
+    };
+    if (split) go(std::true_type{});
+    else go(std::false_type{});
   });
   count_launches(1);
   return e;
