@@ -11,6 +11,7 @@ Sources: "iS-KV reading notes" (zhongzhuzhou.org), Sections 3-5 and Algorithms 1
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 
 import torch
@@ -349,7 +350,7 @@ class _On:
 
 def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> IskvHeads:
     """``t`` ([batch,] row, head, head_dim) as an ``iskv_heads``; its last axis is contiguous."""
-    if t.device != device or not t.is_cuda:
+    if t.get_device() != device.index or device.index is None:
         raise ValueError(f"{name}: all tensors must live on one CUDA device")
     if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype}, expected {dtype}")
@@ -362,7 +363,7 @@ def _heads(t: torch.Tensor, name: str, shape, dtype, device) -> IskvHeads:
 
 
 def _ints(t: torch.Tensor, name: str, shape, device) -> int:
-    if t.device != device or t.dtype is not torch.int32 or not t.is_contiguous() \
+    if t.get_device() != device.index or t.dtype is not torch.int32 or not t.is_contiguous() \
             or t.shape != shape:
         raise ValueError(f"{name} must be a contiguous int32 tensor of shape {shape} on {device}")
     return t.data_ptr()
@@ -376,15 +377,19 @@ def _status_word(t, device):
     return t.data_ptr()
 
 
+def _written(out, t: torch.Tensor, name: str, shape, dtype, device):
+    """``out``, or a contiguous tensor of ``t``'s shape and dtype, with its ``iskv_heads``."""
+    if out is not None:
+        return out, _heads(out, name, shape, dtype, device)
+    out = torch.empty_like(t) if t.is_contiguous() else t.new_empty(shape)
+    row = shape[-2] * shape[-1]
+    return out, IskvHeads(out.data_ptr(), shape[-3] * row, row, shape[-1])
+
+
 def _rank(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} axes, expected {n}")
     return t.shape
-
-
-def _new(t: torch.Tensor) -> torch.Tensor:
-    """A contiguous tensor of ``t``'s shape and dtype."""
-    return torch.empty_like(t) if t.is_contiguous() else t.new_empty(t.shape)
 
 
 def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None, stream=None):
@@ -398,9 +403,7 @@ def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None,
     dt = _dt(x)
     pp = _ints(pos, "pos", (n,), dev)
     with _On(dev, stream) as s:
-        if out is None:
-            out = _new(x)
-        ho = _heads(out, "out", shape, x.dtype, dev)
+        out, ho = _written(out, x, "out", shape, x.dtype, dev)
         _lib.check(_lib.load().iskv_rope(hx, pp, n, heads, hd, theta, inverse, dt, ho, s), "rope")
     return out
 
@@ -425,15 +428,14 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
         if cu_seqlens is not None:
             seqs = max(cu_seqlens.numel() - 1, 0)
             cp = _ints(cu_seqlens, "cu_seqlens", (seqs + 1,), dev)
-        if out is None:
-            out = _new(q)
-        ho = _heads(out, "out", shape, dtype, dev)
+        out, ho = _written(out, q, "out", shape, dtype, dev)
         _lib.check(_lib.load().iskv_prompt_attention(
             hq, hk, hv, cp, seqs, rows, nq, nkv, hd,
             1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, s), "prompt_attention")
     return out
 
 
+@functools.lru_cache(maxsize=256)
 def tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads, head_dim) -> int:
     return int(_lib.load().iskv_tree_attention_workspace_size(n_nodes, n_q_heads, n_kv_heads,
                                                               head_dim))
@@ -463,14 +465,11 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     sw = _status_word(status, dev)
     lib = _lib.load()
     with _On(dev, stream) as s:
-        if out is None:
-            out = _new(q)
-        ho = _heads(out, "out", shape, dtype, dev)
+        out, ho = _written(out, q, "out", shape, dtype, dev)
         if ws is None:
             # A buffer of this call's own, from the stream's pool: calls on several streams and
             # captured graphs never share one.
-            ws = torch.empty(lib.iskv_tree_attention_workspace_size(t, nq, nkv, hd),
-                             dtype=torch.uint8, device=dev)
+            ws = q.new_empty(tree_attention_workspace_size(t, nq, nkv, hd) // q.element_size())
         _lib.check(lib.iskv_tree_attention(
             hq, hkd, hvd, pp, hkc, hvc, npp, b, t, cap, nq, nkv, hd,
             1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, ws.data_ptr(),

@@ -143,6 +143,13 @@ struct TreeLine {
   }
   ISKV_DEV void begin(const DenseArgs &a, int grid, int cta) {
     const int lane = threadIdx.x & 31;
+    if (a.whole) {  // the CTA's number is its unit's
+      blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
+      draft_tiles = (a.nodes + KT - 1) / KT;
+      x = cta;
+      end = cta + 1;
+      return;
+    }
     blocks = (a.nodes * a.group + ROWS - 1) / ROWS;
     draft_tiles = (a.nodes + KT - 1) / KT;
     len0 = lane < a.batch ? cached_rows(a, lane) : 0;
@@ -153,11 +160,30 @@ struct TreeLine {
     x = (int)min((int64_t)total, (int64_t)per * cta);
     end = min(total - x, per) + x;
   }
+  // Everything of entry u.b's idx-th unit but its tile range.
+  ISKV_DEV void place(const DenseArgs &a, int idx, Unit &u) const {
+    u.base = 0;
+    u.cache_tiles = (u.len + KT - 1) / KT;
+    u.n_tiles = u.cache_tiles + draft_tiles;
+    u.kvh = blocks == 1 ? idx : idx / blocks;
+    u.row0 = (idx - u.kvh * blocks) * ROWS;
+    u.n_rows = min(ROWS, a.nodes * a.group - u.row0);
+  }
   // The next unit of the share, or false.
   ISKV_DEV bool next(const DenseArgs &a, Unit &u) {
     if (x >= end) return false;
     const int lane = threadIdx.x & 31;
     int before = 0;
+    if (a.whole) {
+      const int units = a.n_kv * blocks;
+      u.b = x / units;
+      u.len = cached_rows(a, u.b);
+      place(a, x - u.b * units, u);
+      u.t0 = 0;
+      u.t1 = u.n_tiles;
+      ++x;
+      return true;
+    }
     if (a.batch == 1) {
       u.b = 0;
       u.len = __shfl_sync(0xffffffffu, len0, 0);
@@ -180,14 +206,8 @@ struct TreeLine {
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    u.base = 0;
-    u.cache_tiles = (u.len + KT - 1) / KT;
-    u.n_tiles = u.cache_tiles + draft_tiles;
-    const int all_rows = a.nodes * a.group;
-    const int idx = (x - before) / u.n_tiles;
-    u.kvh = blocks == 1 ? idx : idx / blocks;
-    u.row0 = (idx - u.kvh * blocks) * ROWS;
-    u.n_rows = min(ROWS, all_rows - u.row0);
+    const int idx = (x - before) / ((u.len + KT - 1) / KT + draft_tiles);
+    place(a, idx, u);
     u.t0 = x - before - idx * u.n_tiles;
     u.t1 = min(u.n_tiles, u.t0 + (end - x));
     x += u.t1 - u.t0;

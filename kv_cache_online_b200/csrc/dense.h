@@ -21,6 +21,7 @@ struct DenseArgs {
   const int32_t *n_cached;  // tree: [batch] cached rows in use, or NULL (all n_cap)
   const int32_t *parents;   // tree: [batch][nodes]
   int32_t tree;
+  int32_t whole;            // tree: a CTA per unit, nothing to join
   int32_t batch;            // prompt: sequences; tree: batch entries
   int32_t nodes;            // tree: drafted nodes per entry
   int64_t rows;             // prompt: packed rows; tree: cache capacity n_cap

@@ -33,7 +33,7 @@
 
 #include <cudaTypedefs.h>
 
-#include <mutex>
+#include <cstring>
 
 namespace iskv {
 namespace {
@@ -826,39 +826,65 @@ __global__ void __launch_bounds__(384, 1)
 // ------------------------------------------------------------------------------------------------
 // Host
 
+// A driver entry point by name, looked up once.
+template <typename F>
+F driver_fn(const char *name) {
+  void *f = nullptr;
+  cudaDriverEntryPointQueryResult q;
+  if (cudaGetDriverEntryPoint(name, &f, cudaEnableDefault, &q) != cudaSuccess ||
+      q != cudaDriverEntryPointSuccess)
+    return nullptr;
+  return reinterpret_cast<F>(f);
+}
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
-  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *f = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
-  });
+  static const auto fn = driver_fn<PFN_cuTensorMapEncodeTiled_v12000>("cuTensorMapEncodeTiled");
+  return fn;
+}
+PFN_cuTensorMapReplaceAddress_v12000 replace_fn() {
+  static const auto fn = driver_fn<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
   return fn;
 }
 
 // Two-byte rows as a 4-D tensor {head_dim, heads, rows, entries}, box {64, 1, 128, 1}, 128-byte
-// swizzle; what lies outside reads as zero.
+// swizzle; what lies outside reads as zero. The thread's last maps are kept by their shape (a model's
+// layers differ in addresses alone), which spares a short call an encoding of more than 1 us each.
 bool encode(CUtensorMap *m, int32_t &head_on, int32_t &batch_on, const iskv_heads &x, int hd,
             int heads, int64_t rows, int64_t entries, int dtype) {
+  struct Shape {
+    cuuint64_t dims[4], strides[3];
+    int64_t dtype;
+  };
+  constexpr int KEEP = 8;
+  thread_local Shape shapes[KEEP];
+  thread_local CUtensorMap kept[KEEP];
+  thread_local int used = 0, next = 0;
   head_on = heads > 1 && x.head > 0;
   batch_on = entries > 1 && x.batch > 0;
   // Axes that are not walked get length one and any legal stride.
   const cuuint64_t any = (cuuint64_t)(hd + 7) / 8 * 16;
-  cuuint64_t dims[4] = {(cuuint64_t)hd, head_on ? (cuuint64_t)heads : 1, (cuuint64_t)rows,
-                        batch_on ? (cuuint64_t)entries : 1};
-  cuuint64_t strides[3] = {head_on ? (cuuint64_t)x.head * 2 : any,
-                           x.row > 0 ? (cuuint64_t)x.row * 2 : any,
-                           batch_on ? (cuuint64_t)x.batch * 2 : any};
+  Shape s = {{(cuuint64_t)hd, head_on ? (cuuint64_t)heads : 1, (cuuint64_t)rows,
+              batch_on ? (cuuint64_t)entries : 1},
+             {head_on ? (cuuint64_t)x.head * 2 : any, x.row > 0 ? (cuuint64_t)x.row * 2 : any,
+              batch_on ? (cuuint64_t)x.batch * 2 : any},
+             dtype};
+  if (replace_fn())
+    for (int i = 0; i < used; ++i)
+      if (!memcmp(&s, &shapes[i], sizeof s)) {
+        *m = kept[i];
+        return replace_fn()(m, x.data) == CUDA_SUCCESS;
+      }
   cuuint32_t box[4] = {64, 1, KT, 1}, one[4] = {1, 1, 1, 1};
-  return encode_fn()(m, dtype == ISKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                     4, x.data, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                     CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  if (encode_fn()(m, dtype == ISKV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                  4, x.data, s.dims, s.strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  shapes[next] = s;
+  kept[next] = *m;
+  next = (next + 1) % KEEP;
+  if (used < KEEP) ++used;
+  return true;
 }
 
 template <typename T, int HD, int MODE>
@@ -887,7 +913,8 @@ bool dense_tc_takes(const DenseArgs &a) {
          (!a.tree || a.rows == 0 || (fits(a.kc, a.rows > 1) && fits(a.vc, a.rows > 1)));
 }
 
-bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e) {
+bool launch_dense_tc(const DenseArgs &args, cudaStream_t s, cudaError_t &e) {
+  DenseArgs a = args;
   Maps maps = {};
   const int64_t n = a.tree ? a.nodes : a.rows, entries = a.tree ? a.batch : 1;
   bool ok = encode(&maps.k, maps.k_head, maps.k_batch, a.k, a.head_dim, a.n_kv, n, entries, a.dtype) &&
@@ -901,7 +928,13 @@ bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e) {
   if (!ok) return false;
   const bool keys = a.tree && a.nodes * a.group <= 128;
   const int rows = keys ? 128 : 256;
-  const int64_t grid = a.tree ? DENSE_TC_GRID : (a.rows * a.group / rows + a.batch) * (int64_t)a.n_kv;
+  // A tree over a short cache (seven tiles at most and the drafts') is not cut: a unit takes about 0.6
+  // us a tile, the join 4 us and its launch 3.5 us of host time.
+  const int64_t units = (int64_t)a.batch * a.n_kv * ((a.nodes * a.group + rows - 1) / rows);
+  a.whole = a.tree && a.rows <= 7 * KT && units <= 0x7fffffff;
+  const int64_t grid = a.whole  ? units
+                       : a.tree ? DENSE_TC_GRID
+                                : (a.rows * a.group / rows + a.batch) * (int64_t)a.n_kv;
   if (grid > 0x7fffffff) {
     e = cudaErrorInvalidValue;
     return true;
@@ -919,7 +952,8 @@ bool launch_dense_tc(const DenseArgs &a, cudaStream_t s, cudaError_t &e) {
   };
   if (a.dtype == ISKV_F16) type(__half{});
   else type(__nv_bfloat16{});
-  if (e == cudaSuccess && a.tree) e = launch_dense_join(a, (int)grid, rows, KT, s);
+  if (e == cudaSuccess && a.tree && !a.whole)
+    e = launch_dense_join(a, (int)grid, rows, KT, s);
   return true;
 }
 
