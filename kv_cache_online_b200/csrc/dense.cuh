@@ -21,7 +21,8 @@ namespace iskv {
 namespace dense {
 
 // status: one int64 word (or NULL), bit (1 << code).
-ISKV_DEV void report(int64_t *status, int code) {
+// (Out of line: the callers run once per unit, and their instructions come from L2 each time.)
+static __device__ __noinline__ void report(int64_t *status, int code) {
   if (status) atomicOr(reinterpret_cast<unsigned long long *>(status), 1ull << code);
 }
 
@@ -75,15 +76,18 @@ ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   };
   const int mine = blocks(lane);  // the first 32 sequences stay in registers
   int top = mine;
+#pragma unroll 1
   for (int s = 32 + lane; s < a.batch; s += 32) top = max(top, blocks(s));
   top = __reduce_max_sync(0xffffffffu, top);
   auto F = [&](int m) {
     int n = max(mine - m, 0);
+#pragma unroll 1
     for (int s = 32 + lane; s < a.batch; s += 32) n += max(blocks(s) - m, 0);
     return __reduce_add_sync(0xffffffffu, n);
   };
-  if (top == 0 || F(0) <= rank) return false;
-  int lo = 0, hi = top, above = 0;  // F(lo) > rank >= F(hi) = above
+  if (top == 0) return false;
+  int lo = -1, hi = top, above = 0;  // F(lo) > rank >= F(hi) = above, but for lo = -1
+#pragma unroll 1
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2, f = F(mid);
     if (f > rank) {
@@ -93,7 +97,9 @@ ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
       above = f;
     }
   }
+  if (lo < 0) return false;
   int skip = rank - above;  // among the sequences with more than lo blocks
+#pragma unroll 1
   for (int s0 = 0; s0 < a.batch; s0 += 32) {
     const unsigned has = __ballot_sync(0xffffffffu, (s0 == 0 ? mine : blocks(s0 + lane)) > lo);
     const int n = __popc(has);

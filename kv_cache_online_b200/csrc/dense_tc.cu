@@ -374,22 +374,30 @@ __global__ void __launch_bounds__(384, 1)
       // the unit, so that it cannot run ahead of the MMA warp.)
       if (MODE == MODE_KEYS || n_mine > 0) {
         const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-        const uint64_t row_at = reinterpret_cast<uint64_t>(static_cast<const T *>(a.q.data) +
-                                                           at(a.q, entry, row_base + tok, head));
+        // (Rows beyond the tile read its last one and become zero: a load under a condition waits
+        // for the one before it, 0.2 us each.)
+        const int pq = u.row0 + row_off + min(row, max(tile_rows, 1) - 1), tq = pq / a.group;
+        const uint64_t row_at = reinterpret_cast<uint64_t>(
+            static_cast<const T *>(a.q.data) +
+            at(a.q, entry, row_base + tq, (int64_t)u.kvh * a.group + (pq - tq * a.group)));
+        const int ch = ch0 + lane % CW;
+        const uint64_t col_off = (uint64_t)min(ch, a.head_dim / 8 - 1) * 16;
+        const bool col_in = ch * 8 < a.head_dim;
+        const uint4 *src[CW];
         uint4 x[CW];
 #pragma unroll
-        for (int i = 0; i < CW; ++i) {
-          const int r = (32 * i + lane) / CW, ch = ch0 + lane % CW;
-          const uint64_t src = __shfl_sync(0xffffffffu, row_at, r);
-          x[i] = make_uint4(0, 0, 0, 0);
-          if (quad * 32 + r < tile_rows && ch * 8 < a.head_dim)
-            x[i] = *reinterpret_cast<const uint4 *>(src + ch * 16);
-        }
+        for (int i = 0; i < CW; ++i)
+          src[i] = reinterpret_cast<const uint4 *>(
+              __shfl_sync(0xffffffffu, row_at, (32 * i + lane) / CW) + col_off);
+#pragma unroll
+        for (int i = 0; i < CW; ++i) x[i] = *src[i];
 #pragma unroll
         for (int i = 0; i < CW; ++i) {
-          const int r = (32 * i + lane) / CW, ch = ch0 + lane % CW;
-          *reinterpret_cast<uint4 *>(piece(quad * 32 + r, ch)) =
-              make_uint4(x[i].x ^ flip, x[i].y ^ flip, x[i].z ^ flip, x[i].w ^ flip);
+          const int r = quad * 32 + (32 * i + lane) / CW;
+          const uint32_t keep = col_in && r < tile_rows ? 0xffffffffu : 0u;
+          *reinterpret_cast<uint4 *>(piece(r, ch)) =
+              make_uint4((x[i].x ^ flip) & keep, (x[i].y ^ flip) & keep, (x[i].z ^ flip) & keep,
+                         (x[i].w ^ flip) & keep);
         }
         fence_proxy_async_smem();
         __syncwarp();
