@@ -9,7 +9,9 @@
 // rows and walks tiles of 64 keys; thread (ty, tx) holds scores of rows 4 ty + i and keys
 // tx + 16 j, and output columns 4 tx + 64 c, so that a score step reads 8 float4 for 64 FMAs and a
 // value step 4 + HD/16 float4 for HD FMAs, without bank conflicts (row strides of HD + 4 floats).
-// All operands are float32 in shared memory, products and statistics float32.
+// All operands are float32 in shared memory, products and statistics float32. float32 rows whose
+// 16-byte pieces are aligned (HD up to 128) arrive by asynchronous copies, the next tile's under this
+// tile's arithmetic; other rows go through registers (a tile's loads are then waited for).
 #include "dense.cuh"
 #include "profiling.h"
 
@@ -21,10 +23,10 @@ using namespace dense;
 constexpr int ROWS = DENSE_CC_ROWS, KT = 64, NT = 256;
 constexpr float LOG2E = 1.4426950408889634f;
 
-template <int HD>
+template <int HD, int BUF>
 struct Smem {
   static constexpr int LD = HD + 4;
-  float q[ROWS][LD], k[KT][LD], v[KT][LD];
+  float q[ROWS][LD], k[BUF][KT][LD], v[BUF][KT][LD];
   float p[ROWS][KT + 4];
   uint32_t mask[DENSE_MAX_NODES][4];
   Unit unit;
@@ -68,9 +70,28 @@ ISKV_DEV void load_rows(float (*dst)[HD + 4], const T *src, int64_t stride, int 
   }
 }
 
+// The same rows by asynchronous 16-byte copies (zero where there is nothing to read).
+template <int HD>
+ISKV_DEV void copy_rows(float (*dst)[HD + 4], const float *src, int64_t stride, int n, int hd) {
+  constexpr int C = HD / 4;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < KT * C; i += NT) {
+    const int r = i / C, c = i % C * 4;
+    const bool in = r < n && c < hd;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     (uint32_t)__cvta_generic_to_shared(&dst[r][c])),
+                 "l"(in ? src + r * stride + c : src), "r"(in ? 16 : 0)
+                 : "memory");
+  }
+}
+
+template <typename T, int HD, bool VEC>
+constexpr int BUFFERS = std::is_same<T, float>::value && VEC && HD <= 128 ? 2 : 1;
+
 template <typename T, int HD, bool TREE, bool VEC>
-ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
+ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, const Unit &u) {
   constexpr int NC = HD / 64;
+  constexpr bool ASYNC = BUFFERS<T, HD, VEC> == 2;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int hd = a.head_dim;
   // Non-negative factor on the scores; the scale's sign goes into the queries.
@@ -108,17 +129,38 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
       for (int e = 0; e < 4; ++e) o[i][n][e] = 0.f;
   }
 
+  // Keys and values of tile t into buffer `to`.
+  auto fetch = [&](int t, int to) {
+    const bool draft = TREE && t >= u.cache_tiles;
+    const int k0 = (draft ? t - u.cache_tiles : t) * KT, n = min(KT, (draft ? a.nodes : u.len) - k0);
+    const iskv_heads &K = TREE && !draft ? a.kc : a.k, &V = TREE && !draft ? a.vc : a.v;
+    const T *k = static_cast<const T *>(K.data) + at(K, TREE ? u.b : 0, row_base + k0, u.kvh);
+    const T *v = static_cast<const T *>(V.data) + at(V, TREE ? u.b : 0, row_base + k0, u.kvh);
+    if constexpr (ASYNC) {
+      copy_rows<HD>(sm.k[to], k, K.row, n, hd);
+      copy_rows<HD>(sm.v[to], v, V.row, n, hd);
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    } else {
+      load_rows<T, HD, VEC>(sm.k[to], k, K.row, n, hd);
+      load_rows<T, HD, VEC>(sm.v[to], v, V.row, n, hd);
+    }
+  };
+  int buf = 0;
+  if constexpr (ASYNC) fetch(u.t0, 0);
   for (int t = u.t0; t < u.t1; ++t) {
     const bool draft = TREE && t >= u.cache_tiles;
     const int k0 = (draft ? t - u.cache_tiles : t) * KT;  // first key of the tile
     const int n_keys = min(KT, (draft ? a.nodes : u.len) - k0);
-    const iskv_heads &K = TREE && !draft ? a.kc : a.k, &V = TREE && !draft ? a.vc : a.v;
-    __syncthreads();  // the previous tile's keys, values and probabilities are no longer read
-    load_rows<T, HD, VEC>(sm.k, static_cast<const T *>(K.data) +
-                          at(K, TREE ? u.b : 0, row_base + k0, u.kvh), K.row, n_keys, hd);
-    load_rows<T, HD, VEC>(sm.v, static_cast<const T *>(V.data) +
-                          at(V, TREE ? u.b : 0, row_base + k0, u.kvh), V.row, n_keys, hd);
-    __syncthreads();
+    if constexpr (ASYNC) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+      __syncthreads();  // this tile is there, and nobody reads the other buffer any more
+      buf = (t - u.t0) & 1;
+      if (t + 1 < u.t1) fetch(t + 1, buf ^ 1);
+    } else {
+      __syncthreads();  // the previous tile's keys, values and probabilities are no longer read
+      fetch(t, 0);
+      __syncthreads();
+    }
 
     float s[4][4];
 #pragma unroll
@@ -131,7 +173,7 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty * 4 + i][d]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[tx + 16 * j][d]);
+      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[buf][tx + 16 * j][d]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -200,7 +242,7 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD> &sm, const Unit &u) {
         for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
           for (int n = 0; n < NC; ++n) {
-            const float4 v = *reinterpret_cast<const float4 *>(&sm.v[k + kk][tx * 4 + 64 * n]);
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.v[buf][k + kk][tx * 4 + 64 * n]);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
@@ -264,7 +306,7 @@ template <typename T, int HD, bool TREE, bool VEC>
 __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseArgs a) {
   if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) char raw[];
-  Smem<HD> &sm = *reinterpret_cast<Smem<HD> *>(raw);
+  auto &sm = *reinterpret_cast<Smem<HD, BUFFERS<T, HD, VEC>> *>(raw);
   if constexpr (!TREE) {
     if (threadIdx.x < 32) {
       Unit u;
@@ -451,7 +493,7 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
 template <typename T, int HD, bool TREE, bool VEC>
 cudaError_t run(const DenseArgs &a, int grid, cudaStream_t s) {
   auto *kernel = k_dense_cc<T, HD, TREE, VEC>;
-  const int smem = (int)sizeof(Smem<HD>);
+  const int smem = (int)sizeof(Smem<HD, BUFFERS<T, HD, VEC>>);
   static SmemLimit limit;
   cudaError_t e = limit.raise(reinterpret_cast<const void *>(kernel), smem);
   if (e != cudaSuccess) return e;
