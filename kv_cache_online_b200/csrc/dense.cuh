@@ -62,10 +62,10 @@ template <int ROWS>
 ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   const int lane = threadIdx.x & 31;
   if (a.batch == 1) {
-    u.b = 0;
     u.len = seq_len(a, 0, u.base);
     const int n = (int)(((int64_t)u.len * a.group + ROWS - 1) / ROWS);
     if (rank >= n) return false;
+    u.b = 0;
     u.row0 = (n - 1 - rank) * ROWS;
     u.n_rows = min(ROWS, u.len * a.group - u.row0);
     return true;

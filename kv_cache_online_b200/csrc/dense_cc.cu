@@ -117,7 +117,8 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
     }
   }
   int tok[4];  // prompt: the row's token; tree: its node
-  float m[4], l[4], o[4][NC][4];
+  float m[4], l[4];
+  alignas(8) float o[4][NC][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     tok[i] = (u.row0 + min(ty * 4 + i, u.n_rows - 1)) / a.group;
@@ -162,28 +163,35 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
       __syncthreads();
     }
 
-    float s[4][4];
+    // Even and odd columns in the two halves of packed FMAs (half the instructions).
+    float2 acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) s[i][j] = 0.f;
+      for (int j = 0; j < 4; ++j) acc[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
     for (int d = 0; d < HD; d += 4) {
       float4 qv[4], kv[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4 *>(&sm.q[ty * 4 + i][d]);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(&sm.k[buf][tx + 16 * j][d]);
+      for (int j = 0; j < 4; ++j)
+        kv[j] = *reinterpret_cast<const float4 *>(&sm.k[buf][tx + 16 * j][d]);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-          s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-          s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-          s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+          acc[i][j] = __ffma2_rn(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y),
+                                 acc[i][j]);
+          acc[i][j] = __ffma2_rn(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w),
+                                 acc[i][j]);
         }
     }
+    float s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) s[i][j] = acc[i][j].x + acc[i][j].y;
     // Pairs the mask leaves out have p = -1 in shared memory: the value step skips them, so that
     // a value that is not finite cannot reach a row that does not see it.
     const bool masked = n_keys < KT || draft || (!TREE && k0 + KT > first_token(a, u) + 1);
@@ -247,10 +255,9 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
             for (int i = 0; i < 4; ++i) {
               const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
               if (decltype(guarded)::value && w < 0.f) continue;
-              o[i][n][0] = fmaf(w, v.x, o[i][n][0]);
-              o[i][n][1] = fmaf(w, v.y, o[i][n][1]);
-              o[i][n][2] = fmaf(w, v.z, o[i][n][2]);
-              o[i][n][3] = fmaf(w, v.w, o[i][n][3]);
+              float2 *po = reinterpret_cast<float2 *>(o[i][n]);
+              po[0] = __ffma2_rn(make_float2(w, w), make_float2(v.x, v.y), po[0]);
+              po[1] = __ffma2_rn(make_float2(w, w), make_float2(v.z, v.w), po[1]);
             }
           }
         }
@@ -310,11 +317,12 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
   if constexpr (!TREE) {
     if (threadIdx.x < 32) {
       Unit u;
-      u.b = -1;
       if (find_prompt_unit<ROWS>(a, blockIdx.x / a.n_kv, u)) {
         u.kvh = blockIdx.x % a.n_kv;
         u.t0 = 0;
         u.t1 = u.n_tiles = last_token(a, u) / KT + 1;
+      } else {
+        u.b = -1;
       }
       if (threadIdx.x == 0) sm.unit = u;
     }

@@ -217,7 +217,7 @@ def test_prompt_head_layouts(dtype, nq, nkv, hd):
 
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("lens", [[1], [1, 1, 1], [127, 128, 129], [0, 5, 0, 64, 0], [63, 65, 255, 257],
-                                  [2] * 70, [600]])
+                                  [2] * 70, [600], [64], [128], [192]])
 def test_prompt_lengths(dtype, lens):
     run_prompt(sum(lens), dtype, lens, 4, 2, 128)
 
