@@ -136,6 +136,10 @@ iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, cons
   if (empty) return ISKV_OK;
   if (reinterpret_cast<uintptr_t>(cu_seqlens) % 4)
     return fail(ISKV_ERR_ARG, "%s: misaligned cu_seqlens", who);
+  // One block per 64 packed rows and key/value head at most.
+  if ((n_rows * (n_q_heads / n_kv_heads) / 64 + n_seqs) * n_kv_heads >= (int64_t)1 << 31)
+    return fail(ISKV_ERR_SHAPE, "%s: (n_rows * group / 64 + n_seqs) * n_kv_heads must stay below "
+                "2^31", who);
   if (!cu_seqlens && n_seqs != 1)
     return fail(ISKV_ERR_ARG, "%s: cu_seqlens may be null for one sequence only", who);
   if ((n_rows > 1 && out->row == 0) || (n_q_heads > 1 && out->head == 0))

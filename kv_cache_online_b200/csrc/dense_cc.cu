@@ -309,8 +309,11 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
   }
 }
 
+// Two blocks share an SM where their shared memory fits (HD = 64; 128 registers), else one block has
+// all registers: four prompts of 600 tokens at head_dim 64, 95 against 107 us; 2,500 tokens at
+// head_dim 128, 1,634 against 1,520 us.
 template <typename T, int HD, bool TREE, bool VEC>
-__global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseArgs a) {
+__global__ void __launch_bounds__(NT, HD == 64 ? 2 : 1) k_dense_cc(const __grid_constant__ DenseArgs a) {
   if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) char raw[];
   auto &sm = *reinterpret_cast<Smem<HD, BUFFERS<T, HD, VEC>> *>(raw);
@@ -348,16 +351,15 @@ __global__ void __launch_bounds__(NT) k_dense_cc(const __grid_constant__ DenseAr
 }
 
 // A block: 32 rows (lanes) of one unit. SPLIT: its four warps take every fourth part of the unit for
-// the same `per` groups of four columns, with a running maximum each, and add up in shared memory
-// with weights 2^(m_i - max m) (few units of many parts each); otherwise every warp takes all parts
-// for `per` column groups of its own (many units, a few parts each). Latency bound, a few KB per
-// warp: the loads of four parts are in flight together.
-constexpr int JOIN_COLS = 8;
-
+// the same four columns, with a running maximum each, and add up in shared memory with weights
+// 2^(m_i - max m) (few units of many parts each); otherwise every warp takes all parts for 32
+// columns of its own (many units, a few parts each). Latency bound, a few KB per warp: all loads of
+// four parts are in flight together.
 template <typename T, int ROWS, int KT, bool SPLIT>
 __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ DenseArgs a, int grid,
-                                                    int hd_pad, int per) {
-  __shared__ float part[4][2 + 4 * JOIN_COLS][33], factor[5][32];
+                                                    int hd_pad) {
+  constexpr int COLS = SPLIT ? 1 : 8;  // groups of four columns per warp
+  __shared__ float part[4][2 + 4 * COLS][33], factor[5][32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x / 32;
   TreeLine<ROWS, KT> line;
   line.begin(a, grid, 0);
@@ -372,35 +374,38 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int c0 = u0 / line.per, c1 = (u0 + n - 1) / line.per;
   if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
   const int n_rows = min(ROWS, rows_all - blk * ROWS);
-  const int block_cols = SPLIT ? per : 4 * per, all_cols = (a.head_dim + 3) / 4;
-  const int groups = (all_cols + block_cols - 1) / block_cols;
-  const int r = blockIdx.y / groups * 32 + lane;
-  if (r - lane >= n_rows) return;
+  const int all_cols = (a.head_dim + 3) / 4;
+  constexpr int BLOCK_COLS = SPLIT ? 1 : 4 * COLS;
+  const int groups = (all_cols + BLOCK_COLS - 1) / BLOCK_COLS, chunk = blockIdx.y / groups;
+  const int r = chunk * 32 + lane;
+  if (chunk * 32 >= n_rows) return;
   const int rr = min(r, n_rows - 1);
-  const int g0 = blockIdx.y % groups * block_cols + (SPLIT ? 0 : warp * per);
-  const int gn = max(0, min(per, all_cols - g0));  // this warp's column groups
+  const int g0 = (blockIdx.y - chunk * groups) * BLOCK_COLS + (SPLIT ? 0 : warp * COLS);
   const size_t slot_floats = dense_slot_floats(ROWS, hd_pad);
-  // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's share:
-  // slot 0.
-  auto slot = [&](int c) {
-    return static_cast<const float *>(a.ws) + (c == c0 ? 2 * c + 1 : 2 * c) * slot_floats;
-  };
+  const int pr = blk * ROWS + rr, node = pr / a.group;
+  T *const out = static_cast<T *>(a.out.data) +
+                 at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) + g0 * 4;
   // Up to here only the call's inputs were read; the parts need the kernel before this one.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   constexpr int STEP = SPLIT ? 4 : 1;
   float m = -INFINITY, l = 0.f;
-  float4 o[JOIN_COLS];
+  float4 o[COLS];
 #pragma unroll
-  for (int g = 0; g < JOIN_COLS; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int g = 0; g < COLS; ++g) o[g] = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int c = c0 + (SPLIT ? warp : 0); c <= c1; c += 4 * STEP) {
     float w[4], li[4];
-    float4 v[4];
+    float4 v[4][COLS];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float *s = slot(min(c + STEP * i, c1));
+      // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's
+      // share: slot 0.
+      const int ci = min(c + STEP * i, c1);
+      const float *s = static_cast<const float *>(a.ws) + (ci == c0 ? 2 * ci + 1 : 2 * ci) * slot_floats;
       w[i] = s[(size_t)ROWS * hd_pad + rr];
       li[i] = s[(size_t)ROWS * (hd_pad + 1) + rr];
-      v[i] = reinterpret_cast<const float4 *>(s)[min(g0, all_cols - 1) * ROWS + rr];
+#pragma unroll
+      for (int g = 0; g < COLS; ++g)
+        v[i][g] = reinterpret_cast<const float4 *>(s)[min(g0 + g, all_cols - 1) * ROWS + rr];
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -415,59 +420,43 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
     m = mn;
     l *= f;
 #pragma unroll
+    for (int g = 0; g < COLS; ++g) o[g] = make_float4(o[g].x * f, o[g].y * f, o[g].z * f, o[g].w * f);
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
       // A part that saw nothing has m = -inf and l = 0 (its O may be anything); with m = -inf and
       // another l, not-a-number scores alone were seen.
-      w[i] = w[i] == -INFINITY && li[i] == 0.f ? -1.f : ex2(w[i] - ref);
-      if (!(w[i] < 0.f)) l = fmaf(li[i], w[i], l);
-    }
+      if (w[i] == -INFINITY && li[i] == 0.f) continue;
+      const float e = ex2(w[i] - ref);
+      l = fmaf(li[i], e, l);
 #pragma unroll
-    for (int g = 0; g < JOIN_COLS; ++g) {
-      if (g >= gn) break;
-      if (g > 0) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          v[i] = reinterpret_cast<const float4 *>(slot(min(c + STEP * i, c1)))[(g0 + g) * ROWS + rr];
-      }
-      o[g].x *= f;
-      o[g].y *= f;
-      o[g].z *= f;
-      o[g].w *= f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (w[i] < 0.f) continue;
-        o[g].x = fmaf(v[i].x, w[i], o[g].x);
-        o[g].y = fmaf(v[i].y, w[i], o[g].y);
-        o[g].z = fmaf(v[i].z, w[i], o[g].z);
-        o[g].w = fmaf(v[i].w, w[i], o[g].w);
+      for (int g = 0; g < COLS; ++g) {
+        o[g].x = fmaf(v[i][g].x, e, o[g].x);
+        o[g].y = fmaf(v[i][g].y, e, o[g].y);
+        o[g].z = fmaf(v[i][g].z, e, o[g].z);
+        o[g].w = fmaf(v[i][g].w, e, o[g].w);
       }
     }
   }
   // Rows leave through shared memory with neighbouring columns in neighbouring lanes. l = 0: padding
   // nodes, which came as parts that saw nothing.
-  const int row0 = blk * ROWS + r - lane, rows = min(32, n_rows - (r - lane)), width = 4 * gn;
-  auto put = [&](int row, int x, float v) {
-    const int col = g0 * 4 + x;
-    if (col >= a.head_dim) return;
-    const int pr = row0 + row, node = pr / a.group;
-    static_cast<T *>(a.out.data)[at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) +
-                                 col] = from_f<T>(v);
-  };
-  const float scale = SPLIT ? 1.f : l != 0.f ? 1.f / l : 0.f;
 #pragma unroll
-  for (int g = 0; g < JOIN_COLS; ++g) {
-    if (g >= gn) break;
-    const bool keep = SPLIT || l != 0.f;
-    part[warp][2 + 4 * g][lane] = keep ? o[g].x * scale : 0.f;
-    part[warp][3 + 4 * g][lane] = keep ? o[g].y * scale : 0.f;
-    part[warp][4 + 4 * g][lane] = keep ? o[g].z * scale : 0.f;
-    part[warp][5 + 4 * g][lane] = keep ? o[g].w * scale : 0.f;
+  for (int g = 0; g < COLS; ++g) {
+    part[warp][2 + 4 * g][lane] = o[g].x;
+    part[warp][3 + 4 * g][lane] = o[g].y;
+    part[warp][4 + 4 * g][lane] = o[g].z;
+    part[warp][5 + 4 * g][lane] = o[g].w;
   }
+  const int rows = min(32, n_rows - chunk * 32);
   if constexpr (!SPLIT) {
+    part[warp][0][lane] = l;
     __syncwarp();
-    for (int i = lane; i < rows * width; i += 32) {
-      const int row = i / width, x = i - row * width;
-      put(row, x, part[warp][2 + x][row]);
+    const bool in = g0 * 4 + lane < a.head_dim;
+#pragma unroll 4
+    for (int row = 0; row < rows; ++row) {
+      T *dst = reinterpret_cast<T *>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), row));
+      const float sum = part[warp][0][row], v = part[warp][2 + lane][row];
+      if (in) dst[lane] = from_f<T>(sum != 0.f ? v / sum : 0.f);
     }
   } else {
     part[warp][0][lane] = m;
@@ -487,14 +476,14 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
       factor[4][lane] = sum;
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < rows * width; i += 128) {
-      const int row = i / width, x = i - row * width;
-      const float sum = factor[4][row];
-      float v = 0.f;
+    // Eight rows of four columns per warp.
+    const int row = warp * 8 + lane / 4, x = lane & 3;
+    T *dst = reinterpret_cast<T *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(out), row));
+    const float sum = factor[4][row];
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w) v += part[w][2 + x][row] * factor[w][row];
-      put(row, x, sum != 0.f ? v / sum : 0.f);
-    }
+    for (int w = 0; w < 4; ++w) v += part[w][2 + x][row] * factor[w][row];
+    if (row < rows && g0 * 4 + x < a.head_dim) dst[x] = from_f<T>(sum != 0.f ? v / sum : 0.f);
   }
 }
 
@@ -522,12 +511,10 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
   cudaLaunchConfig_t cfg = {};
   const int cols = (a.head_dim + 3) / 4;
   const int64_t units = (int64_t)a.batch * a.n_kv * blocks;
-  // `grid` shares over `units` units: with fewer than about 40 units (four parts or more each) the
-  // parts of a unit are split over warps, one column group per block; otherwise whole rows per
-  // block (64 units of 192 rows and three to four parts: 24 us split, 9 us not).
+  // `grid` shares over `units` units: up to about 40 units (four parts or more each) the parts of a
+  // unit are split over warps, four columns per block; otherwise 128 columns per block.
   const bool split = units * 4 <= grid;
-  const int per = split ? 1 : (cols + 3) / 4 > JOIN_COLS ? JOIN_COLS : (cols + 3) / 4;
-  const int block_cols = split ? per : 4 * per;
+  const int block_cols = split ? 1 : 32;
   cfg.gridDim = dim3((unsigned)units, (unsigned)(chunks * ((cols + block_cols - 1) / block_cols)));
   cfg.blockDim = dim3(128);
   cfg.stream = s;
@@ -539,9 +526,9 @@ cudaError_t launch_dense_join(const DenseArgs &a, int grid, int rows, int keys, 
     using T = decltype(tag);
     auto go = [&](auto sp) {
       constexpr bool S = decltype(sp)::value;
-      e = keys == 64    ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64, S>, a, grid, pad, per)
-          : rows == 128 ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128, S>, a, grid, pad, per)
-                        : cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128, S>, a, grid, pad, per);
+      e = keys == 64    ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 64, 64, S>, a, grid, pad)
+          : rows == 128 ? cudaLaunchKernelEx(&cfg, k_dense_join<T, 128, 128, S>, a, grid, pad)
+                        : cudaLaunchKernelEx(&cfg, k_dense_join<T, 256, 128, S>, a, grid, pad);
     };
     if (split) go(std::true_type{});
     else go(std::false_type{});

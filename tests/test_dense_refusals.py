@@ -63,7 +63,7 @@ def test_rope_refuses(want, kw):
     (SHAPE, {"seqs": 4097}), (ARG, {"cu": None}), (ARG, {"cu": P + 1}), (ARG, {"status": P + 4}),
     (ARG, {"q": (0, 1, 1, 0)}), (ARG, {"k": (0, 1, 1, P + 1)}), (SHAPE, {"v": (0, 1, -1, P)}),
     (SHAPE, {"k": (0, 1 << 36, 1, P)}), (SHAPE, {"out": (0, 0, 128, P)}),
-    (SHAPE, {"out": (0, 1024, 0, P)}),
+    (SHAPE, {"out": (0, 1024, 0, P)}), (SHAPE, {"rows": 1 << 24, "nq": 16384, "nkv": 256}),
 ])
 def test_prompt_attention_refuses(want, kw):
     L, lib = _lib()
@@ -79,7 +79,8 @@ def test_prompt_attention_refuses(want, kw):
     (ARG, {"parents": P + 2}), (ARG, {"ncached": P + 2}), (ARG, {"status": P + 4}),
     (ARG, {"kc": (0, 1, 1, 0)}), (ARG, {"vd": (0, 1, 1, 0)}), (SHAPE, {"q": (-1, 1, 1, P)}),
     (SHAPE, {"out": (0, 1024, 128, P)}), (SHAPE, {"out": (4096, 0, 128, P)}),
-    (SHAPE, {"out": (4096, 1024, 0, P)}), (WORKSPACE, {"ws": None}), (WORKSPACE, {"ws": P + 16}),
+    (SHAPE, {"out": (4096, 1024, 0, P)}),
+    (SHAPE, {"batch": 4096, "nodes": 128, "nq": 512, "cap": 1 << 20}), (WORKSPACE, {"ws": None}), (WORKSPACE, {"ws": P + 16}),
     (WORKSPACE, {"ws_bytes": 4096}),
 ])
 def test_tree_attention_refuses(want, kw):
