@@ -1,6 +1,7 @@
 // Dense attention on the tensor cores (tcgen05): bf16 and fp16, head_dim up to 128.
 //
-// Mathematics: one pass over the keys in tiles of 128. Per row, with x = scale log2(e) q.k,
+// Mathematics: one pass over the keys in tiles of 128, half a tile at a time. Per row, with
+// x = scale log2(e) q.k,
 //   S = Q K^T;  m: reference maximum;  P = 2^(x - m + bias);  l += sum P;  O += P V;  out = O / l.
 // m only moves when a row's maximum exceeds it by more than 8 (a factor 2^8 in P, harmless in the
 // float32 sums): then l and O are multiplied by 2^(m - m'). P enters the second product in the
@@ -8,15 +9,22 @@
 // bf16 and 6 for fp16, which moves fp16's subnormal range from 2^-14 to 2^-20 of the largest
 // weight. l sums the unrounded float32 values. S, m, l and O are float32.
 //
-// What bounds it: per SM and tile of 128 x 128 pairs at head_dim 128, 1,024 clocks of tensor core
-// (4,096 multiply-adds a clock) and 1,024 clocks of the exponential unit (16 a clock), so both have
-// to run all the time: two independent streams per CTA, each with its own S and O in tensor
-// memory, alternate between the tensor core and their own softmax warpgroup. Long caches with few
-// rows are bound by HBM instead (the keys and values cross once).
+// Streams: two per CTA, each with its own softmax warpgroup, MMA warp, two S and one O, so that one
+// stream's exponentials run under the other's products. MODE_PROMPT and MODE_ROWS give each stream
+// its own 128 rows over the same key tiles; MODE_KEYS (a tree of at most 128 packed rows) gives both
+// the same rows and every other tile, and adds the two results up at the end.
 //
-// Streams: MODE_PROMPT and MODE_ROWS give each stream its own 128 rows over the same key tiles;
-// MODE_KEYS (a tree of at most 128 packed rows) gives both the same rows and every other tile, and
-// adds the two results up at the end.
+// What bounds it: for 64 keys of both streams at head_dim 128 the products take 1,288 clocks of an SM
+// (P V: 4 MMAs of 65; S: 8 MMAs of N = 64, which take 48 and not 32 because the A operand comes from
+// shared memory), the exponentials 1,034 (a warp's 32 in 8). Measured 1,350 over a 32,768-token
+// prompt: 6.4-7.5 ms = 1.17-1.37 PFLOP/s with the clock at 1.4 to 1.7 GHz under the power cap. Short
+// units pay about 5 us before the first S (unit lookup 1.5, queries 2.5) and 2.5 us after the last.
+// Trees with few rows are bound by HBM instead (the cache crosses once).
+//
+// One S of 128 keys per stream left the softmax waiting for two products in a row (4,400 clocks for
+// 128 keys; 2,700 now). Also measured and not kept: two threads per row (8 % slower: the exchange of
+// the maxima), part of the exponentials as a polynomial on the FMA pipe (no gain once the products
+// bound it), ex2.approx.f16x2 (the rate per element is the same).
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row; P goes back to tensor memory in S's
 // place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring;
@@ -61,7 +69,7 @@ struct Ctl {
   // is not refilled before the MMA has read it.
   uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
   uint64_t q_full[2], s_full[2][2], p_full[2][2];  // [stream][half of the tile's keys]
-  uint64_t o_full[2];      // a phase per product P V; read only where the one before is known complete
+  uint64_t o_full[2];      // a phase per product P V; read only where the one before is complete
   uint64_t o_last[2];      // a phase per unit: its last P V
   uint64_t both, drain;
   uint32_t tmem;
@@ -77,7 +85,7 @@ struct Cfg {
   static constexpr int ROWS = 128 * NQ;                     // packed rows of a unit
   static constexpr int AHEAD = MODE == MODE_KEYS ? 2 : 1;   // key tiles ahead of the value tile
   // As many ring slots as fit beside the query tiles in 227 KB, at most 8.
-  static constexpr int REST = (int)sizeof(Ctl) + (MODE == MODE_KEYS ? 2048 : 0);  // + m, l of the streams
+  static constexpr int REST = (int)sizeof(Ctl) + (MODE == MODE_KEYS ? 2048 : 0);  // + m, l
   static constexpr int FIT = (232448 - REST - NQ * TILE) / TILE;
   static constexpr int SLOTS = FIT < MAX_SLOTS ? FIT : MAX_SLOTS;
   static constexpr int SMEM = NQ * TILE + SLOTS * TILE + REST;
@@ -118,6 +126,7 @@ ISKV_DEV float max3(float a, float b, float c) {
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
+
 template <typename T>
 ISKV_DEV uint32_t pack2(float a, float b) {
   if constexpr (std::is_same<T, __half>::value) {
@@ -600,225 +609,225 @@ __global__ void __launch_bounds__(384, 1)
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
-  if (warp == 8) {
-    // ------------------------------------------------------------------------- loads
-    RingPos pos;
-    int issued = 0;
-    bool ok = true;
-    while (ok && walk.next(a, u)) {
+    if (warp == 8) {
+      // ------------------------------------------------------------------------- loads
+      RingPos pos;
+      int issued = 0;
+      bool ok = true;
+      while (ok && walk.next(a, u)) {
+        if (lane == 0) {
+          const int n = u.t1 - u.t0;
+          auto load = [&](int t, bool value) {
+            if (!ok) return;
+            if (!mbar_wait(&ctl.kv_empty[pos.slot], pos.phase ^ 1, abort, WAIT_NS)) {
+              ok = false;
+              ctl.abort = 1;
+              return;
+            }
+            const bool cache = TREE && t < u.cache_tiles;
+            const CUtensorMap *map = cache ? (value ? &maps.vc : &maps.kc) : (value ? &maps.v : &maps.k);
+            const int head = u.kvh * (cache ? (value ? maps.vc_head : maps.kc_head)
+                                            : (value ? maps.v_head : maps.k_head));
+            const int entry = TREE ? u.b * (cache ? (value ? maps.vc_batch : maps.kc_batch)
+                                                  : (value ? maps.v_batch : maps.k_batch))
+                                   : 0;
+            const int row = TREE ? (cache ? t : t - u.cache_tiles) * KT : (int)u.base + t * KT;
+            const uint32_t dst = ring_smem + pos.slot * C::TILE;
+            mbar_arrive_expect_tx(&ctl.kv_full[pos.slot], C::TILE);
+            if (value && hidden_from<MODE>(u, t) < KT) mbar_arrive(&ctl.v_req[pos.slot]);
+            for (int s = 0; s < C::SLABS; ++s)
+              tma_load_4d(dst + s * 16384, map, s * 64, head, row, entry, &ctl.kv_full[pos.slot]);
+            ++issued;
+            pos.next(C::SLOTS);
+          };
+          for (int i = 0; i < C::AHEAD && i < n; ++i) load(u.t0 + i, false);
+          for (int i = 0; i < n; ++i) {
+            load(u.t0 + i, true);
+            if (i + C::AHEAD < n) load(u.t0 + i + C::AHEAD, false);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0);
+      }
       if (lane == 0) {
-        const int n = u.t1 - u.t0;
-        auto load = [&](int t, bool value) {
-          if (!ok) return;
-          if (!mbar_wait(&ctl.kv_empty[pos.slot], pos.phase ^ 1, abort, WAIT_NS)) {
-            ok = false;
-            ctl.abort = 1;
-            return;
+        // Copies in flight land before the CTA ends (after a timeout nobody else waits for them): the
+        // last use of every slot that was issued.
+        RingPos p;
+        for (int i = 0; i < issued; ++i) {
+          if (i + C::SLOTS >= issued) {
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(&ctl.kv_full[p.slot], p.phase) && globaltimer() - t0 < WAIT_NS) {
+            }
           }
-          const bool cache = TREE && t < u.cache_tiles;
-          const CUtensorMap *map = cache ? (value ? &maps.vc : &maps.kc) : (value ? &maps.v : &maps.k);
-          const int head = u.kvh * (cache ? (value ? maps.vc_head : maps.kc_head)
-                                          : (value ? maps.v_head : maps.k_head));
-          const int entry = TREE ? u.b * (cache ? (value ? maps.vc_batch : maps.kc_batch)
-                                                : (value ? maps.v_batch : maps.k_batch))
-                                 : 0;
-          const int row = TREE ? (cache ? t : t - u.cache_tiles) * KT : (int)u.base + t * KT;
-          const uint32_t dst = ring_smem + pos.slot * C::TILE;
-          mbar_arrive_expect_tx(&ctl.kv_full[pos.slot], C::TILE);
-          if (value && hidden_from<MODE>(u, t) < KT) mbar_arrive(&ctl.v_req[pos.slot]);
-          for (int s = 0; s < C::SLABS; ++s)
-            tma_load_4d(dst + s * 16384, map, s * 64, head, row, entry, &ctl.kv_full[pos.slot]);
-          ++issued;
-          pos.next(C::SLOTS);
-        };
-        for (int i = 0; i < C::AHEAD && i < n; ++i) load(u.t0 + i, false);
-        for (int i = 0; i < n; ++i) {
-          load(u.t0 + i, true);
-          if (i + C::AHEAD < n) load(u.t0 + i + C::AHEAD, false);
+          p.next(C::SLOTS);
         }
       }
-      ok = __shfl_sync(0xffffffffu, (int)ok, 0);
-    }
-    if (lane == 0) {
-      // Copies in flight land before the CTA ends (after a timeout nobody else waits for them): the
-      // last use of every slot that was issued.
-      RingPos p;
-      for (int i = 0; i < issued; ++i) {
-        if (i + C::SLOTS >= issued) {
-          const uint64_t t0 = globaltimer();
-          while (!mbar_try_wait(&ctl.kv_full[p.slot], p.phase) && globaltimer() - t0 < WAIT_NS) {
-          }
+    } else if (warp < 11) {
+      // ------------------------------------------------------------------------- MMAs
+      // A warp per stream: what it takes to see that a P has come and to issue the next products is
+      // longer than the products, and two warps overlap it (one warp for both: 1,740 clocks for 64
+      // keys of both streams at head_dim 128). The whole warp walks through the loops in step and one
+      // lane issues: addresses and descriptors then stay in uniform registers, where the MMA takes
+      // them from. Both warps follow every ring slot, used or not, so that neither loses a phase.
+      constexpr uint32_t ID_S = idesc<T>(128, KT / 2, false), ID_O = idesc<T>(128, HD, true);
+      const int st = warp - 9;
+      const uint32_t leader = elect_one();
+      RingPos pos;
+      uint32_t ph_q = 0, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per half
+      bool ok = true;
+      const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : st) * C::TILE);
+      const uint32_t s_tm = 128 * st, o_tm = O_COL + HD * st;
+      auto tile_at = [&](int slot) { return ring_smem + slot * C::TILE; };
+      // S over half h of a key tile.
+      auto scores = [&](int h, int slot) {
+        const uint64_t kd = sw128_desc(tile_at(slot) + h * 8192);
+#pragma unroll
+        for (int k = 0; k < HD / 16; ++k) {
+          const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
+          mma_ss(leader, s_tm + 64 * h, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
         }
-        p.next(C::SLOTS);
-      }
-    }
-  } else if (warp < 11) {
-    // ------------------------------------------------------------------------- MMAs
-    // A warp per stream: what it takes to see that a P has come and to issue the next products is
-    // longer than the products, and two warps overlap it (one warp for both: 1,740 clocks for 64
-    // keys of both streams at head_dim 128). The whole warp walks through the loops in step and one
-    // lane issues: addresses and descriptors then stay in uniform registers, where the MMA takes
-    // them from. Both warps follow every ring slot, used or not, so that neither loses a phase.
-    constexpr uint32_t ID_S = idesc<T>(128, KT / 2, false), ID_O = idesc<T>(128, HD, true);
-    const int st = warp - 9;
-    const uint32_t leader = elect_one();
-    RingPos pos;
-    uint32_t ph_q = 0, ph_v = 0, ph_p = 0;  // ph_v: a bit per slot; ph_p: per half
-    bool ok = true;
-    const uint64_t qd = sw128_desc(q_smem + (MODE == MODE_KEYS ? 0 : st) * C::TILE);
-    const uint32_t s_tm = 128 * st, o_tm = O_COL + HD * st;
-    auto tile_at = [&](int slot) { return ring_smem + slot * C::TILE; };
-    // S over half h of a key tile.
-    auto scores = [&](int h, int slot) {
-      const uint64_t kd = sw128_desc(tile_at(slot) + h * 8192);
-#pragma unroll
-      for (int k = 0; k < HD / 16; ++k) {
-        const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        mma_ss(leader, s_tm + 64 * h, desc_add(qd, off), desc_add(kd, off), ID_S, k > 0);
-      }
-      commit(leader, &ctl.s_full[st][h]);
-    };
-    // P V over half h of a value tile, once the softmax has written P.
-    auto values = [&](int h, int slot, bool first, bool last) {
-      if (!warp_wait(&ctl.p_full[st][h], ph_p >> h & 1, abort)) return false;
-      ph_p ^= 1u << h;
-      fence_after_sync();
-      const uint64_t vd = sw128_mn_desc(tile_at(slot) + h * 8192, 16384);
-#pragma unroll
-      for (int k = 0; k < KT / 32; ++k)
-        mma_ts(leader, o_tm, s_tm + 64 * h + 8 * k, desc_add(vd, k * 2048), ID_O, !first || k > 0);
-      commit(leader, &ctl.o_full[st]);
-      if (last) commit(leader, &ctl.o_last[st]);
-      return true;
-    };
-    // Two S per stream: the next half's scores are under way while the softmax works on this
-    // half's. S(i + 2) goes where P(i) was, behind P(i) V(i) in the same pipe.
-    while (ok && walk.next(a, u)) {
-      const int n = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0);
-      const int n_mine = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, st), 0);
-      if (MODE == MODE_KEYS || n_mine > 0) {
-        ok = warp_wait(&ctl.q_full[MODE == MODE_KEYS ? 0 : st], ph_q, abort);
-        ph_q ^= 1;
+        commit(leader, &ctl.s_full[st][h]);
+      };
+      // P V over half h of a value tile, once the softmax has written P.
+      auto values = [&](int h, int slot, bool first, bool last) {
+        if (!warp_wait(&ctl.p_full[st][h], ph_p >> h & 1, abort)) return false;
+        ph_p ^= 1u << h;
         fence_after_sync();
-      }
-      for (int i = 0; ok && i < C::AHEAD && i < n; ++i) {
-        ok = warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
-        if (!ok) break;
-        if (MODE != MODE_KEYS || i == st) {
-          if (n_mine > 0) scores(0, pos.slot);
-          if (n_mine > 1) scores(1, pos.slot);
+        const uint64_t vd = sw128_mn_desc(tile_at(slot) + h * 8192, 16384);
+#pragma unroll
+        for (int k = 0; k < KT / 32; ++k)
+          mma_ts(leader, o_tm, s_tm + 64 * h + 8 * k, desc_add(vd, k * 2048), ID_O, !first || k > 0);
+        commit(leader, &ctl.o_full[st]);
+        if (last) commit(leader, &ctl.o_last[st]);
+        return true;
+      };
+      // Two S per stream: the next half's scores are under way while the softmax works on this
+      // half's. S(i + 2) goes where P(i) was, behind P(i) V(i) in the same pipe.
+      while (ok && walk.next(a, u)) {
+        const int n = __shfl_sync(0xffffffffu, u.t1 - u.t0, 0);
+        const int n_mine = __shfl_sync(0xffffffffu, stream_halves<MODE>(a, u, st), 0);
+        if (MODE == MODE_KEYS || n_mine > 0) {
+          ok = warp_wait(&ctl.q_full[MODE == MODE_KEYS ? 0 : st], ph_q, abort);
+          ph_q ^= 1;
+          fence_after_sync();
         }
-        commit(leader, &ctl.kv_empty[pos.slot]);
-        pos.next(C::SLOTS);
-      }
-      for (int i = 0; ok && i < n; ++i) {
-        const int v_slot = pos.slot;
-        ok = warp_wait(&ctl.kv_full[v_slot], pos.phase, abort);
-        pos.next(C::SLOTS);
-        if (ok && hidden_from<MODE>(u, u.t0 + i) < KT) {
-          ok = warp_wait(&ctl.v_ok[v_slot], ph_v >> v_slot & 1, abort);
-          ph_v ^= 1u << v_slot;
-        }
-        const bool more = i + C::AHEAD < n;
-        const int k_slot = pos.slot;
-        if (ok && more) {
-          ok = warp_wait(&ctl.kv_full[k_slot], pos.phase, abort);
+        for (int i = 0; ok && i < C::AHEAD && i < n; ++i) {
+          ok = warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
+          if (!ok) break;
+          if (MODE != MODE_KEYS || i == st) {
+            if (n_mine > 0) scores(0, pos.slot);
+            if (n_mine > 1) scores(1, pos.slot);
+          }
+          commit(leader, &ctl.kv_empty[pos.slot]);
           pos.next(C::SLOTS);
         }
-        if (!ok) break;
-        if (MODE != MODE_KEYS || (i & 1) == st) {
-          const int b = MODE == MODE_KEYS ? i - st : 2 * i;  // the stream's first half of the tile
-          if (b < n_mine) {
-            ok = values(0, v_slot, b == 0, b + 1 == n_mine);
-            if (ok && b + 2 < n_mine) scores(0, k_slot);
+        for (int i = 0; ok && i < n; ++i) {
+          const int v_slot = pos.slot;
+          ok = warp_wait(&ctl.kv_full[v_slot], pos.phase, abort);
+          pos.next(C::SLOTS);
+          if (ok && hidden_from<MODE>(u, u.t0 + i) < KT) {
+            ok = warp_wait(&ctl.v_ok[v_slot], ph_v >> v_slot & 1, abort);
+            ph_v ^= 1u << v_slot;
           }
-          if (ok && b + 1 < n_mine) {
-            ok = values(1, v_slot, false, b + 2 == n_mine);
-            if (ok && b + 3 < n_mine) scores(1, k_slot);
+          const bool more = i + C::AHEAD < n;
+          const int k_slot = pos.slot;
+          if (ok && more) {
+            ok = warp_wait(&ctl.kv_full[k_slot], pos.phase, abort);
+            pos.next(C::SLOTS);
           }
           if (!ok) break;
-        }
-        commit(leader, &ctl.kv_empty[v_slot]);
-        if (more) commit(leader, &ctl.kv_empty[k_slot]);
-      }
-    }
-    // Every MMA and commit has completed before the CTA gives its tensor memory back.
-    commit(leader, &ctl.drain);
-    if (lane == 0) {
-      const uint64_t t0 = globaltimer();
-      while (!mbar_try_wait(&ctl.drain, 0) && globaltimer() - t0 < WAIT_NS) {
-      }
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------------------- value check
-    RingPos pos;
-    uint32_t ph_req = 0;  // a bit per slot
-    bool ok = true;
-    while (ok && walk.next(a, u)) {
-      const int n = u.t1 - u.t0;
-      for (int i = 0; i < C::AHEAD && i < n; ++i) pos.next(C::SLOTS);
-      for (int i = 0; i < n && ok; ++i) {
-        const int t = u.t0 + i;
-        const int r0 = max(0, hidden_from<MODE>(u, t));
-        const int r1 = !TREE || t < u.cache_tiles ? KT : a.nodes;
-        if (r0 < KT) {
-          ok = warp_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort) &&
-               warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
-          ph_req ^= 1u << pos.slot;
-          if (!ok) {
-            ctl.abort = 1;
-            break;
-          }
-          // A row is 8 16-byte pieces of each 64-column slab, whatever their swizzled order.
-          char *tile = base + (C::NQ + pos.slot) * C::TILE;
-          const int p0 = r0 * 8, p1 = r1 * 8;
-          uint32_t top = 0;
-          for (int s = 0; s < C::SLABS; ++s)
-#pragma unroll 4
-            for (int p = p0 + lane; p < p1; p += 32) {
-              const uint4 x = *reinterpret_cast<const uint4 *>(tile + s * 16384 + p * 16);
-              top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                           __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+          if (MODE != MODE_KEYS || (i & 1) == st) {
+            const int b = MODE == MODE_KEYS ? i - st : 2 * i;  // the stream's first half of the tile
+            if (b < n_mine) {
+              ok = values(0, v_slot, b == 0, b + 1 == n_mine);
+              if (ok && b + 2 < n_mine) scores(0, k_slot);
             }
-          constexpr uint32_t E = EXP_BITS<T> & 0xffffu;
-          if (__any_sync(0xffffffffu, (top & 0xffffu) >= E || (top >> 16) >= E)) {
-            // Cache rows beyond the valid ones, and rows behind a sequence, are seen by nobody.
-            const int seen_end = TREE ? (t < u.cache_tiles ? 0 : a.nodes) : u.len - t * KT;
-            bool seen = false;
-            for (int s = 0; s < C::SLABS; ++s)
-              for (int p = p0 + lane; p < p1; p += 32) {
-                uint4 *at16 = reinterpret_cast<uint4 *>(tile + s * 16384 + p * 16);
-                uint4 x = *at16;
-                uint32_t *wd = reinterpret_cast<uint32_t *>(&x);
-                bool hit = false;
-                for (int e = 0; e < 4; ++e) {
-                  if ((wd[e] & E) == E) {
-                    wd[e] &= 0xffff0000u;
-                    hit = true;
-                  }
-                  if ((wd[e] >> 16 & E) == E) {
-                    wd[e] &= 0xffffu;
-                    hit = true;
-                  }
-                }
-                if (hit) {
-                  *at16 = x;
-                  seen |= p / 8 < seen_end;
-                }
-              }
-            if (__any_sync(0xffffffffu, seen) && lane == 0)
-              *(volatile int *)&ctl.fix[walk.count & 7] = walk.count;
-            fence_proxy_async_smem();
+            if (ok && b + 1 < n_mine) {
+              ok = values(1, v_slot, false, b + 2 == n_mine);
+              if (ok && b + 3 < n_mine) scores(1, k_slot);
+            }
+            if (!ok) break;
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ctl.v_ok[pos.slot]);
+          commit(leader, &ctl.kv_empty[v_slot]);
+          if (more) commit(leader, &ctl.kv_empty[k_slot]);
         }
-        pos.next(C::SLOTS);
-        if (i + C::AHEAD < n) pos.next(C::SLOTS);
+      }
+      // Every MMA and commit has completed before the CTA gives its tensor memory back.
+      commit(leader, &ctl.drain);
+      if (lane == 0) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&ctl.drain, 0) && globaltimer() - t0 < WAIT_NS) {
+        }
+      }
+      __syncwarp();
+    } else {
+      // ------------------------------------------------------------------------- value check
+      RingPos pos;
+      uint32_t ph_req = 0;  // a bit per slot
+      bool ok = true;
+      while (ok && walk.next(a, u)) {
+        const int n = u.t1 - u.t0;
+        for (int i = 0; i < C::AHEAD && i < n; ++i) pos.next(C::SLOTS);
+        for (int i = 0; i < n && ok; ++i) {
+          const int t = u.t0 + i;
+          const int r0 = max(0, hidden_from<MODE>(u, t));
+          const int r1 = !TREE || t < u.cache_tiles ? KT : a.nodes;
+          if (r0 < KT) {
+            ok = warp_wait(&ctl.v_req[pos.slot], ph_req >> pos.slot & 1, abort) &&
+                 warp_wait(&ctl.kv_full[pos.slot], pos.phase, abort);
+            ph_req ^= 1u << pos.slot;
+            if (!ok) {
+              ctl.abort = 1;
+              break;
+            }
+            // A row is 8 16-byte pieces of each 64-column slab, whatever their swizzled order.
+            char *tile = base + (C::NQ + pos.slot) * C::TILE;
+            const int p0 = r0 * 8, p1 = r1 * 8;
+            uint32_t top = 0;
+            for (int s = 0; s < C::SLABS; ++s)
+#pragma unroll 4
+              for (int p = p0 + lane; p < p1; p += 32) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(tile + s * 16384 + p * 16);
+                top = __vmaxu2(top, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                             __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+              }
+            constexpr uint32_t E = EXP_BITS<T> & 0xffffu;
+            if (__any_sync(0xffffffffu, (top & 0xffffu) >= E || (top >> 16) >= E)) {
+              // Cache rows beyond the valid ones, and rows behind a sequence, are seen by nobody.
+              const int seen_end = TREE ? (t < u.cache_tiles ? 0 : a.nodes) : u.len - t * KT;
+              bool seen = false;
+              for (int s = 0; s < C::SLABS; ++s)
+                for (int p = p0 + lane; p < p1; p += 32) {
+                  uint4 *at16 = reinterpret_cast<uint4 *>(tile + s * 16384 + p * 16);
+                  uint4 x = *at16;
+                  uint32_t *wd = reinterpret_cast<uint32_t *>(&x);
+                  bool hit = false;
+                  for (int e = 0; e < 4; ++e) {
+                    if ((wd[e] & E) == E) {
+                      wd[e] &= 0xffff0000u;
+                      hit = true;
+                    }
+                    if ((wd[e] >> 16 & E) == E) {
+                      wd[e] &= 0xffffu;
+                      hit = true;
+                    }
+                  }
+                  if (hit) {
+                    *at16 = x;
+                    seen |= p / 8 < seen_end;
+                  }
+                }
+              if (__any_sync(0xffffffffu, seen) && lane == 0)
+                *(volatile int *)&ctl.fix[walk.count & 7] = walk.count;
+              fence_proxy_async_smem();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ctl.v_ok[pos.slot]);
+          }
+          pos.next(C::SLOTS);
+          if (i + C::AHEAD < n) pos.next(C::SLOTS);
+        }
       }
     }
-  }
   }
 
   __syncwarp();
