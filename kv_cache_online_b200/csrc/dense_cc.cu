@@ -95,7 +95,7 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int hd = a.head_dim;
   // Non-negative factor on the scores; the scale's sign goes into the queries.
-  const float c = fabsf(a.scale) * LOG2E;
+  const float c = fmaxf(fabsf(a.scale) * LOG2E, 1e-30f);  // (not 0: masked scores are -inf)
   const int64_t row_base = TREE ? 0 : u.base;
 
   for (int i = threadIdx.x; i < ROWS * HD; i += NT) {
@@ -117,12 +117,12 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
     }
   }
   int tok[4];  // prompt: the row's token; tree: its node
-  float m[4], l[4];
+  float raw[4], m[4], l[4];  // m = c max s (raw), l: sum of the weights
   alignas(8) float o[4][NC][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     tok[i] = (u.row0 + min(ty * 4 + i, u.n_rows - 1)) / a.group;
-    m[i] = -INFINITY;
+    raw[i] = m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
     for (int n = 0; n < NC; ++n)
@@ -211,21 +211,24 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float top = -INFINITY;
+      float top = raw[i];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        s[i][j] = seen >> (i * 4 + j) & 1 ? s[i][j] * c : -INFINITY;
+        s[i][j] = seen >> (i * 4 + j) & 1 ? s[i][j] : -INFINITY;
         top = fmaxf(top, s[i][j]);
       }
 #pragma unroll
       for (int w = 8; w > 0; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
-      const float mn = fmaxf(m[i], top);
-      const float ref = mn == -INFINITY ? 0.f : mn;
+      // One rounding of s c - m (of s c alone it would be that of the larger number); m's own
+      // rounding is common to the row's weights.
+      raw[i] = top;
+      const float mn = top == -INFINITY ? -INFINITY : top * c;
+      const float ref = top == -INFINITY ? 0.f : mn;
       const float alpha = ex2(m[i] - ref);  // 0 while nothing was seen
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float p = ex2(s[i][j] - ref);
+        const float p = ex2(fmaf(s[i][j], c, -ref));
         const bool see = seen >> (i * 4 + j) & 1;
         if (see) sum += p;
         sm.p[ty * 4 + i][tx + 16 * j] = see ? p : -1.f;
