@@ -4,8 +4,8 @@
 // r = (token, query head of the group) = (r / group, r % group), so that a tile's rows share every
 // key and value and a single token still fills `group` rows.
 //
-// Prompt: a unit is (sequence, key/value head, block of ROWS packed rows) and runs over the keys
-// up to its last token. CTAs take units in descending row-block index over all sequences: the longest
+// Prompt: a unit is (sequence, key/value head, block of ROWS packed rows) and runs over the keys up
+// to its last token. CTAs take units in descending row-block index over all sequences: the longest
 // runs first, the short ones fill up behind them.
 //
 // Tree: a unit is (batch entry, key/value head, row block); its keys are the cached rows, in tiles
@@ -37,7 +37,7 @@ struct Unit {
   int cache_tiles;  // tree: key tiles over the cache (the drafted nodes' follow)
   int n_tiles;
   int t0, t1;
-  int open;       // first key row that not every row of the unit sees (prompt: token; tree: cached row)
+  int open;       // first key (prompt: token; tree: cached row) that some row must not see
 };
 
 // Rows [lo, hi) of sequence s; an inconsistent entry counts as empty and is reported.
@@ -134,8 +134,9 @@ ISKV_DEV int cached_rows(const DenseArgs &a, int b) {
   return n;
 }
 
-// The line of a tree call's tiles (fewer than 2^31, which the entry point checks) and a CTA's way along
-// its share of it (whole-warp calls). Shares are `per` tiles each, the last ones may be empty.
+// The line of a tree call's tiles (fewer than 2^31, which the entry point checks) and a CTA's way
+// along its share of it (whole-warp calls). Shares are `per` tiles each, the last ones may be
+// empty.
 template <int ROWS, int KT>
 struct TreeLine {
   int blocks, draft_tiles;
@@ -222,10 +223,10 @@ struct TreeLine {
 };
 
 // Whole warp: bits of the nodes that each lane's node i sees, given its entry's parents: itself and
-// its ancestors. par[i] is the index of an earlier node, or -1 (a child of the last cached token); an
-// entry below -1 is padding. Padding, a node whose chain reaches padding, and an entry that is not
-// below its own index (reported) see nothing. The parents sit in four registers of the warp, a step
-// up the chain is a shuffle.
+// its ancestors. par[i] is the index of an earlier node, or -1 (a child of the last cached token);
+// an entry below -1 is padding. Padding, a node whose chain reaches padding, and an entry that is
+// not below its own index (reported) see nothing. The parents sit in four registers of the warp, a
+// step up the chain is a shuffle.
 ISKV_DEV void node_mask(const DenseArgs &a, const int32_t *par, int i, uint32_t (&m)[4]) {
   const int lane = threadIdx.x & 31;
   int p[4];

@@ -1,6 +1,6 @@
 // Dense attention around the compressed cache: whole packed prompts (causal) and trees of drafted
-// tokens over a dense cache, and the rotary embedding both need. Argument blocks and host launchers;
-// the C-ABI checks are in dense_api.cu.
+// tokens over a dense cache, and the rotary embedding both need. Argument blocks and host
+// launchers; the C-ABI checks are in dense_api.cu.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -206,7 +206,8 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   if (st == ISKV_OK) st = check_status_word(status, who);
   if (st != ISKV_OK) return st;
   if (empty) return ISKV_OK;
-  // The line of key tiles is counted in 32 bits; no kernel's tiles or row blocks are smaller than 64.
+  // The line of key tiles is counted in 32 bits; no kernel's tiles or row blocks are smaller than
+  // 64.
   const int64_t blocks = (n_nodes * (n_q_heads / n_kv_heads) + 63) / 64;
   if ((int64_t)batch * n_kv_heads * blocks >= ((int64_t)1 << 31) / (n_cap / 64 + 3))
     return fail(ISKV_ERR_SHAPE, "%s: batch * n_kv_heads * row blocks * key tiles must stay below "
@@ -223,7 +224,8 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   if (reinterpret_cast<uintptr_t>(ws) % 256)
     return fail(ISKV_ERR_WORKSPACE, "%s: workspace must be 256-byte aligned", who);
   if (ws_bytes < need)
-    return fail(ISKV_ERR_WORKSPACE, "%s: workspace too small (%zu < %zu bytes)", who, ws_bytes, need);
+    return fail(ISKV_ERR_WORKSPACE, "%s: workspace too small (%zu < %zu bytes)", who, ws_bytes,
+                need);
   DenseArgs a = {};
   a.q = walked(q, batch, n_nodes, n_q_heads);
   a.k = walked(k_draft, batch, n_nodes, n_kv_heads);

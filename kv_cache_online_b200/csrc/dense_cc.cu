@@ -6,12 +6,12 @@
 //   O' = O 2^(m - m') + sum_j p_j v_j;  out = O / l.
 //
 // FP32-FMA bound: 4 hd flops per visible pair on 128 lanes per SM. A block of 256 threads owns 64
-// rows and walks tiles of 64 keys; thread (ty, tx) holds scores of rows 4 ty + i and keys
-// tx + 16 j, and output columns 4 tx + 64 c, so that a score step reads 8 float4 for 64 FMAs and a
-// value step 4 + HD/16 float4 for HD FMAs, without bank conflicts (row strides of HD + 4 floats).
-// All operands are float32 in shared memory, products and statistics float32. float32 rows whose
-// 16-byte pieces are aligned (HD up to 128) arrive by asynchronous copies, the next tile's under this
-// tile's arithmetic; other rows go through registers (a tile's loads are then waited for).
+// rows and walks tiles of 64 keys; thread (ty, tx) holds scores of rows 4 ty + i and keys tx + 16
+// j, and output columns 4 tx + 64 c, so that a score step reads 8 float4 for 64 FMAs and a value
+// step 4 + HD/16 float4 for HD FMAs, without bank conflicts (row strides of HD + 4 floats). All
+// operands are float32 in shared memory, products and statistics float32. float32 rows whose
+// 16-byte pieces are aligned (HD up to 128) arrive by asynchronous copies, the next tile's under
+// this tile's arithmetic; other rows go through registers (a tile's loads are then waited for).
 #include "dense.cuh"
 #include "profiling.h"
 
@@ -133,7 +133,8 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
   // Keys and values of tile t into buffer `to`.
   auto fetch = [&](int t, int to) {
     const bool draft = TREE && t >= u.cache_tiles;
-    const int k0 = (draft ? t - u.cache_tiles : t) * KT, n = min(KT, (draft ? a.nodes : u.len) - k0);
+    const int k0 = (draft ? t - u.cache_tiles : t) * KT;
+    const int n = min(KT, (draft ? a.nodes : u.len) - k0);
     const iskv_heads &K = TREE && !draft ? a.kc : a.k, &V = TREE && !draft ? a.vc : a.v;
     const T *k = static_cast<const T *>(K.data) + at(K, TREE ? u.b : 0, row_base + k0, u.kvh);
     const T *v = static_cast<const T *>(V.data) + at(V, TREE ? u.b : 0, row_base + k0, u.kvh);
@@ -312,11 +313,12 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
   }
 }
 
-// Two blocks share an SM where their shared memory fits (HD = 64; 128 registers), else one block has
-// all registers: four prompts of 600 tokens at head_dim 64, 95 against 107 us; 2,500 tokens at
+// Two blocks share an SM where their shared memory fits (HD = 64; 128 registers), else one block
+// has all registers: four prompts of 600 tokens at head_dim 64, 95 against 107 us; 2,500 tokens at
 // head_dim 128, 1,634 against 1,520 us.
 template <typename T, int HD, bool TREE, bool VEC>
-__global__ void __launch_bounds__(NT, HD == 64 ? 2 : 1) k_dense_cc(const __grid_constant__ DenseArgs a) {
+__global__ void __launch_bounds__(NT, HD == 64 ? 2 : 1)
+    k_dense_cc(const __grid_constant__ DenseArgs a) {
   if constexpr (TREE) asm volatile("griddepcontrol.launch_dependents;");
   extern __shared__ __align__(16) char raw[];
   auto &sm = *reinterpret_cast<Smem<HD, BUFFERS<T, HD, VEC>> *>(raw);
@@ -353,8 +355,8 @@ __global__ void __launch_bounds__(NT, HD == 64 ? 2 : 1) k_dense_cc(const __grid_
   }
 }
 
-// A block: 32 rows (lanes) of one unit. SPLIT: its four warps take every fourth part of the unit for
-// the same four columns, with a running maximum each, and add up in shared memory with weights
+// A block: 32 rows (lanes) of one unit. SPLIT: its four warps take every fourth part of the unit
+// for the same four columns, with a running maximum each, and add up in shared memory with weights
 // 2^(m_i - max m) (few units of many parts each); otherwise every warp takes all parts for 32
 // columns of its own (many units, a few parts each). Latency bound, a few KB per warp: all loads of
 // four parts are in flight together.
@@ -403,7 +405,8 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
       // The part with the unit's first tile is in its CTA's slot 1, the others open their CTA's
       // share: slot 0.
       const int ci = min(c + STEP * i, c1);
-      const float *s = static_cast<const float *>(a.ws) + (ci == c0 ? 2 * ci + 1 : 2 * ci) * slot_floats;
+      const float *s =
+          static_cast<const float *>(a.ws) + (ci == c0 ? 2 * ci + 1 : 2 * ci) * slot_floats;
       w[i] = s[(size_t)ROWS * hd_pad + rr];
       li[i] = s[(size_t)ROWS * (hd_pad + 1) + rr];
 #pragma unroll
@@ -423,7 +426,8 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
     m = mn;
     l *= f;
 #pragma unroll
-    for (int g = 0; g < COLS; ++g) o[g] = make_float4(o[g].x * f, o[g].y * f, o[g].z * f, o[g].w * f);
+    for (int g = 0; g < COLS; ++g)
+      o[g] = make_float4(o[g].x * f, o[g].y * f, o[g].z * f, o[g].w * f);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       // A part that saw nothing has m = -inf and l = 0 (its O may be anything); with m = -inf and
@@ -440,8 +444,8 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
       }
     }
   }
-  // Rows leave through shared memory with neighbouring columns in neighbouring lanes. l = 0: padding
-  // nodes, which came as parts that saw nothing.
+  // Rows leave through shared memory with neighbouring columns in neighbouring lanes. l = 0:
+  // padding nodes, which came as parts that saw nothing.
 #pragma unroll
   for (int g = 0; g < COLS; ++g) {
     part[warp][2 + 4 * g][lane] = o[g].x;
@@ -557,7 +561,8 @@ cudaError_t launch_dense_cc(const DenseArgs &a, cudaStream_t s) {
       constexpr int HD = decltype(hd)::value;
       auto mode = [&](auto tree) {
         constexpr bool TREE = decltype(tree)::value;
-        e = vec ? run<T, HD, TREE, true>(a, (int)grid, s) : run<T, HD, TREE, false>(a, (int)grid, s);
+        e = vec ? run<T, HD, TREE, true>(a, (int)grid, s)
+                : run<T, HD, TREE, false>(a, (int)grid, s);
       };
       if (a.tree) mode(std::true_type{});
       else mode(std::false_type{});

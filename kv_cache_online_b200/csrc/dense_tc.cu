@@ -11,27 +11,27 @@
 //
 // Streams: two per CTA, each with its own softmax warpgroup, MMA warp, two S and one O, so that one
 // stream's exponentials run under the other's products. MODE_PROMPT and MODE_ROWS give each stream
-// its own 128 rows over the same key tiles; MODE_KEYS (a tree of at most 128 packed rows) gives both
-// the same rows and every other tile, and adds the two results up at the end.
+// its own 128 rows over the same key tiles; MODE_KEYS (a tree of at most 128 packed rows) gives
+// both the same rows and every other tile, and adds the two results up at the end.
 //
-// What bounds it: for 64 keys of both streams at head_dim 128 the products take 1,288 clocks of an SM
-// (P V: 4 MMAs of 65; S: 8 MMAs of N = 64, which take 48 and not 32 because the A operand comes from
-// shared memory), the exponentials 1,034 (a warp's 32 in 8). Measured 1,350 over a 32,768-token
-// prompt: 6.4-7.5 ms = 1.17-1.37 PFLOP/s with the clock at 1.4 to 1.7 GHz under the power cap. Short
-// units pay about 5 us before the first S (unit lookup 1.5, queries 2.5) and 2.5 us after the last.
-// Trees with few rows are bound by HBM instead (the cache crosses once).
+// What bounds it: for 64 keys of both streams at head_dim 128 the products take 1,288 clocks of an
+// SM (P V: 4 MMAs of 65; S: 8 MMAs of N = 64, which take 48 and not 32 because the A operand comes
+// from shared memory), the exponentials 1,034 (a warp's 32 in 8). Measured 1,350 over a
+// 32,768-token prompt: 6.4-7.5 ms = 1.17-1.37 PFLOP/s with the clock at 1.4 to 1.7 GHz under the
+// power cap. Short units pay about 5 us before the first S (unit lookup 1.5, queries 2.5) and 2.5
+// us after the last. Trees with few rows are bound by HBM instead (the cache crosses once).
 //
 // One S of 128 keys per stream left the softmax waiting for two products in a row (4,400 clocks for
-// 128 keys; 2,700 now). Also measured and not kept: two threads per row (8 % slower: the exchange of
-// the maxima), part of the exponentials as a polynomial on the FMA pipe (no gain once the products
-// bound it), ex2.approx.f16x2 (the rate per element is the same).
+// 128 keys; 2,700 now). Also measured and not kept: two threads per row (8 % slower: the exchange
+// of the maxima), an eighth or a quarter of the exponentials as a polynomial on the FMA pipe (4 to
+// 7 % slower at head_dim 128, no gain at 64), ex2.approx.f16x2 (the rate per element is the same).
 //
 // Warps: 0-3 and 4-7 softmax of stream 0 and 1 (thread = row; P goes back to tensor memory in S's
-// place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring;
-// 9 and 10 issue the MMAs of stream 0 and 1; 11 looks through value tiles of which some row must not
-// see some key, and replaces what is not finite by zero before the MMA reads it (0 * NaN would reach
-// every row); if such a value is seen by some row, the epilogue adds it to exactly the rows that
-// see it.
+// place, as the A operand of the second product); 8 loads key and value tiles by TMA into a ring; 9
+// and 10 issue the MMAs of stream 0 and 1; 11 looks through value tiles of which some row must not
+// see some key, and replaces what is not finite by zero before the MMA reads it (0 * NaN would
+// reach every row); if such a value is seen by some row, the epilogue adds it to exactly the rows
+// that see it.
 //
 // Tensor memory (512 columns): two S of 128 x 64 per stream at 0 and 128 (P over the first half of
 // each), O0, O1 at 256.
@@ -65,8 +65,8 @@ struct Maps {
 struct Ctl {
   uint64_t kv_full[MAX_SLOTS], kv_empty[MAX_SLOTS];
   // A value tile that needs the check: the loader has issued it (until then the parity of kv_full
-  // says nothing about it), the check has passed it. A phase each per checked use of the slot, which
-  // is not refilled before the MMA has read it.
+  // says nothing about it), the check has passed it. A phase each per checked use of the slot,
+  // which is not refilled before the MMA has read it.
   uint64_t v_req[MAX_SLOTS], v_ok[MAX_SLOTS];
   uint64_t q_full[2], s_full[2][2], p_full[2][2];  // [stream][half of the tile's keys]
   uint64_t o_full[2];      // a phase per product P V; read only where the one before is complete
@@ -209,7 +209,8 @@ ISKV_DEV int stream_halves(const DenseArgs &a, const Unit &u, int s) {
     return u.n_rows <= 128 * s
                ? 0
                : (u.row0 + min(u.n_rows, 128 * (s + 1)) - 1) / a.group / (KT / 2) + 1;
-  const int n = u.t1 - u.t0, tiles = MODE == MODE_KEYS ? (n + 1 - s) / 2 : u.n_rows > 128 * s ? n : 0;
+  const int n = u.t1 - u.t0;
+  const int tiles = MODE == MODE_KEYS ? (n + 1 - s) / 2 : u.n_rows > 128 * s ? n : 0;
   if (tiles == 0) return 0;
   // The stream's last tile may have nothing in its second half.
   const int t = MODE == MODE_KEYS ? u.t0 + 2 * tiles - 2 + s : u.t1 - 1;
@@ -625,7 +626,8 @@ __global__ void __launch_bounds__(384, 1)
               return;
             }
             const bool cache = TREE && t < u.cache_tiles;
-            const CUtensorMap *map = cache ? (value ? &maps.vc : &maps.kc) : (value ? &maps.v : &maps.k);
+            const CUtensorMap *map =
+                cache ? (value ? &maps.vc : &maps.kc) : (value ? &maps.v : &maps.k);
             const int head = u.kvh * (cache ? (value ? maps.vc_head : maps.kc_head)
                                             : (value ? maps.v_head : maps.k_head));
             const int entry = TREE ? u.b * (cache ? (value ? maps.vc_batch : maps.kc_batch)
@@ -649,8 +651,8 @@ __global__ void __launch_bounds__(384, 1)
         ok = __shfl_sync(0xffffffffu, (int)ok, 0);
       }
       if (lane == 0) {
-        // Copies in flight land before the CTA ends (after a timeout nobody else waits for them): the
-        // last use of every slot that was issued.
+        // Copies in flight land before the CTA ends (after a timeout nobody else waits for them):
+        // the last use of every slot that was issued.
         RingPos p;
         for (int i = 0; i < issued; ++i) {
           if (i + C::SLOTS >= issued) {
@@ -662,12 +664,12 @@ __global__ void __launch_bounds__(384, 1)
         }
       }
     } else if (warp < 11) {
-      // ------------------------------------------------------------------------- MMAs
-      // A warp per stream: what it takes to see that a P has come and to issue the next products is
-      // longer than the products, and two warps overlap it (one warp for both: 1,740 clocks for 64
-      // keys of both streams at head_dim 128). The whole warp walks through the loops in step and one
-      // lane issues: addresses and descriptors then stay in uniform registers, where the MMA takes
-      // them from. Both warps follow every ring slot, used or not, so that neither loses a phase.
+      // ------------------------------------------------------------------------- MMAs A warp per
+      // stream: what it takes to see that a P has come and to issue the next products is longer
+      // than the products, and two warps overlap it (one warp for both: 1,740 clocks for 64 keys of
+      // both streams at head_dim 128). The whole warp walks through the loops in step and one lane
+      // issues: addresses and descriptors then stay in uniform registers, where the MMA takes them
+      // from. Both warps follow every ring slot, used or not, so that neither loses a phase.
       constexpr uint32_t ID_S = idesc<T>(128, KT / 2, false), ID_O = idesc<T>(128, HD, true);
       const int st = warp - 9;
       const uint32_t leader = elect_one();
@@ -695,7 +697,8 @@ __global__ void __launch_bounds__(384, 1)
         const uint64_t vd = sw128_mn_desc(tile_at(slot) + h * 8192, 16384);
 #pragma unroll
         for (int k = 0; k < KT / 32; ++k)
-          mma_ts(leader, o_tm, s_tm + 64 * h + 8 * k, desc_add(vd, k * 2048), ID_O, !first || k > 0);
+          mma_ts(leader, o_tm, s_tm + 64 * h + 8 * k, desc_add(vd, k * 2048), ID_O,
+                 !first || k > 0);
         commit(leader, &ctl.o_full[st]);
         if (last) commit(leader, &ctl.o_last[st]);
         return true;
@@ -736,7 +739,8 @@ __global__ void __launch_bounds__(384, 1)
           }
           if (!ok) break;
           if (MODE != MODE_KEYS || (i & 1) == st) {
-            const int b = MODE == MODE_KEYS ? i - st : 2 * i;  // the stream's first half of the tile
+            // the stream's first half of the tile
+            const int b = MODE == MODE_KEYS ? i - st : 2 * i;
             if (b < n_mine) {
               ok = values(0, v_slot, b == 0, b + 1 == n_mine);
               if (ok && b + 2 < n_mine) scores(0, k_slot);
@@ -858,13 +862,15 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 PFN_cuTensorMapReplaceAddress_v12000 replace_fn() {
-  static const auto fn = driver_fn<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
+  static const auto fn =
+      driver_fn<PFN_cuTensorMapReplaceAddress_v12000>("cuTensorMapReplaceAddress");
   return fn;
 }
 
 // Two-byte rows as a 4-D tensor {head_dim, heads, rows, entries}, box {64, 1, 128, 1}, 128-byte
-// swizzle; what lies outside reads as zero. The thread's last maps are kept by their shape (a model's
-// layers differ in addresses alone), which spares a short call an encoding of more than 1 us each.
+// swizzle; what lies outside reads as zero. The thread's last maps are kept by their shape (a
+// model's layers differ in addresses alone), which spares a short call an encoding of more than 1
+// us each.
 bool encode(CUtensorMap *m, int32_t &head_on, int32_t &batch_on, const iskv_heads &x, int hd,
             int heads, int64_t rows, int64_t entries, int dtype) {
   struct Shape {
@@ -934,8 +940,9 @@ bool launch_dense_tc(const DenseArgs &args, cudaStream_t s, cudaError_t &e) {
   DenseArgs a = args;
   Maps maps = {};
   const int64_t n = a.tree ? a.nodes : a.rows, entries = a.tree ? a.batch : 1;
-  bool ok = encode(&maps.k, maps.k_head, maps.k_batch, a.k, a.head_dim, a.n_kv, n, entries, a.dtype) &&
-            encode(&maps.v, maps.v_head, maps.v_batch, a.v, a.head_dim, a.n_kv, n, entries, a.dtype);
+  bool ok =
+      encode(&maps.k, maps.k_head, maps.k_batch, a.k, a.head_dim, a.n_kv, n, entries, a.dtype) &&
+      encode(&maps.v, maps.v_head, maps.v_batch, a.v, a.head_dim, a.n_kv, n, entries, a.dtype);
   if (a.tree && a.rows > 0)
     ok = ok &&
          encode(&maps.kc, maps.kc_head, maps.kc_batch, a.kc, a.head_dim, a.n_kv, a.rows, entries,
@@ -945,8 +952,8 @@ bool launch_dense_tc(const DenseArgs &args, cudaStream_t s, cudaError_t &e) {
   if (!ok) return false;
   const bool keys = a.tree && a.nodes * a.group <= 128;
   const int rows = keys ? 128 : 256;
-  // A tree over a short cache (seven tiles at most and the drafts') is not cut: a unit takes about 0.6
-  // us a tile, the join 4 us and its launch 3.5 us of host time.
+  // A tree over a short cache (seven tiles at most and the drafts') is not cut: a unit takes about
+  // 0.6 us a tile, the join 4 us and its launch 3.5 us of host time.
   const int64_t units = (int64_t)a.batch * a.n_kv * ((a.nodes * a.group + rows - 1) / rows);
   a.whole = a.tree && a.rows <= 7 * KT && units <= 0x7fffffff;
   const int64_t grid = a.whole  ? units

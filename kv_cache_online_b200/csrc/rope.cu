@@ -5,9 +5,9 @@
 //
 // Angles: w_j = theta^(-2j/hd) / 2 pi turns per position as a 0.64 fixed-point fraction; pos * w_j
 // modulo 2^64 is the angle modulo one turn, exact but for w_j's own rounding (pos * 2^-65 turns).
-// The two top bits after rounding pick the quadrant, the rest (|r| <= 1/8 turn) goes to the sine and
-// cosine: CUDA's sincospif for float32, the hardware's for two-byte elements, whose own rounding
-// (2^-12 and up) is far above the hardware's 2^-21.
+// The two top bits after rounding pick the quadrant, the rest (|r| <= 1/8 turn) goes to the sine
+// and cosine: CUDA's sincospif for float32, the hardware's for two-byte elements, whose own
+// rounding (2^-12 and up) is far above the hardware's 2^-21.
 //
 // HBM bound: 2 * n * heads * hd elements. A thread owns 16 bytes at j and at j + hd/2 of one row,
 // forms their angles once and walks the heads with four pairs of loads in flight; short calls
