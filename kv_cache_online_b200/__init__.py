@@ -449,7 +449,9 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     child of the last cached token, below -1 for padding; ``k_cache``, ``v_cache`` (batch, n_cap,
     n_kv, head_dim) with ``n_cached`` (batch,) int32 rows in use (None: all). Queries and keys are
     rotated. Node ``i`` sees the cached rows, itself and its ancestors; padding gives zeros. One node
-    with parent -1 is plain decoding. Returns the outputs in ``q``'s shape and dtype."""
+    with parent -1 is plain decoding. Returns the outputs in ``q``'s shape and dtype. ``status``: an
+    int64 tensor that collects error bits; ``ws``: a workspace to use instead of a buffer of the
+    call's own (calls that may overlap need one each)."""
     shape = _rank(q, "q", 4)
     b, t, nq, hd = shape
     _, cap, nkv, _ = _rank(k_cache, "k_cache", 4)

@@ -362,6 +362,18 @@ def test_tree_scales(dtype):
     run_tree(8, dtype, 6, [700], 4, 1, 64, scale=3.0)
 
 
+@pytest.mark.parametrize("dtype", DT)
+def test_tree_units_cut_between_ctas(dtype):
+    """Caches with room for more than seven tiles are cut into equal shares: units of one and of two
+    row blocks, in two and in many parts, several whole ones per share, padding among the rows."""
+    run_tree(40, dtype, 100, [1500, 3, 1100], 12, 4, 64)
+    run_tree(41, dtype, 128, [2000], 2, 1, 128, live=[90])
+    run_tree(42, dtype, 100, [5, 0, 260, 131, 40, 77, 10, 1] * 8, 3, 1, 64, cap=1000)
+    run_tree(43, dtype, 20, [90, 0, 300, 999], 2, 1, 64, live=[20, 0, 7, 13], cap=1000)
+    run_tree(44, dtype, 6, [1000] * 50, 6, 2, 80, cap=1001)
+    run_tree(45, dtype, 1, [1200, 7], 64, 1, 33)
+
+
 def test_tree_long_cache():
     run_tree(10, torch.bfloat16, 3, [20011], 2, 1, 128)
     run_tree(11, torch.float16, 2, [9000, 17], 2, 2, 64)
@@ -389,9 +401,10 @@ def test_tree_bad_parents_and_lengths_are_reported(dtype):
                                       (torch.float32, 64), (torch.bfloat16, 12)])
 @pytest.mark.parametrize("group", [2, 40])
 @pytest.mark.parametrize("bad", [NAN, float("inf")])
-def test_tree_branch_that_is_not_finite_stays_in_its_branch(dtype, hd, group, bad):
+@pytest.mark.parametrize("cap", [200, 1000])
+def test_tree_branch_that_is_not_finite_stays_in_its_branch(dtype, hd, group, bad, cap):
     K = kv()
-    q, kd, vd, kc, vc = tree_inputs(4, dtype, 1, 6, 200, group, 1, hd)
+    q, kd, vd, kc, vc = tree_inputs(4, dtype, 1, 6, cap, group, 1, hd)
     par = [[-1, 0, 0, 1, 2, -2]]  # branches 0-1-3 and 0-2-4, one padding node
     vd[0, 5], kd[0, 5], q[0, 5] = NAN, NAN, NAN
     clean = np64(vd)
