@@ -377,21 +377,23 @@ __global__ void __launch_bounds__(128) k_dense_join(const __grid_constant__ Dens
   const int n = (cached_rows(a, b) + KT - 1) / KT + line.draft_tiles;
   const int u0 = before + (kvh * line.blocks + blk) * n;
   const int c0 = u0 / line.per, c1 = (u0 + n - 1) / line.per;
-  if (c0 == c1) return;  // one CTA had all of it and wrote the rows itself
   const int n_rows = min(ROWS, rows_all - blk * ROWS);
   const int all_cols = (a.head_dim + 3) / 4;
   constexpr int BLOCK_COLS = SPLIT ? 1 : 4 * COLS;
   const int groups = (all_cols + BLOCK_COLS - 1) / BLOCK_COLS, chunk = blockIdx.y / groups;
   const int r = chunk * 32 + lane;
-  if (chunk * 32 >= n_rows) return;
   const int rr = min(r, n_rows - 1);
   const int g0 = (blockIdx.y - chunk * groups) * BLOCK_COLS + (SPLIT ? 0 : warp * COLS);
   const size_t slot_floats = dense_slot_floats(ROWS, hd_pad);
   const int pr = blk * ROWS + rr, node = pr / a.group;
   T *const out = static_cast<T *>(a.out.data) +
                  at(a.out, b, node, (int64_t)kvh * a.group + (pr - node * a.group)) + g0 * 4;
-  // Up to here only the call's inputs were read; the parts need the kernel before this one.
+  // Up to here only the call's inputs were read; the parts need the kernel before this one. Every
+  // block waits, those without rows to join too: later work on the stream is ordered behind this
+  // kernel alone, and this one behind the kernel before it only by the wait.
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (c0 == c1) return;  // one CTA had all of the unit and wrote its rows itself
+  if (chunk * 32 >= n_rows) return;
   constexpr int STEP = SPLIT ? 4 : 1;
   float m = -INFINITY, l = 0.f;
   float4 o[COLS];
