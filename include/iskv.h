@@ -333,9 +333,10 @@ iskv_status iskv_rope(const iskv_heads *x, const int32_t *pos, int64_t n, int32_
  * q and k arrive rotated. Rows outside every sequence are neither read into a result nor written;
  * a value or key that is not finite reaches only the rows that attend to it.
  * q, out       [n_rows][n_q_heads][head_dim] dtype.  k, v [n_rows][n_kv_heads][head_dim].
- * cu_seqlens   [n_seqs + 1] int32 device, not decreasing, inside [0, n_rows]; a sequence whose two
- *              entries break that counts as empty and records ISKV_ERR_SHAPE in *status. NULL with
- *              n_seqs == 1: one sequence of all rows.
+ * cu_seqlens   [n_seqs + 1] int32 device, not decreasing, inside [0, n_rows]. From the first sequence
+ *              on whose two entries break that, all count as empty (nothing of theirs is written),
+ *              and ISKV_ERR_SHAPE is recorded in *status. NULL with n_seqs == 1: one sequence of
+ *              all rows.
  * status       device int64, or NULL: bits (1 << code) are OR-ed in (ISKV_ERR_SHAPE,
  *              ISKV_ERR_TIMEOUT).
  * out must not overlap the inputs. 0 <= n_rows <= 2^24, 0 <= n_seqs <= 4096, n_q_heads a multiple

@@ -412,8 +412,8 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
     """Causal attention over whole prompts packed one behind another: ``q`` (rows, n_q, head_dim),
     ``k`` and ``v`` (rows, n_kv, head_dim), rotated; sequence ``s`` is rows ``cu_seqlens[s]`` to
     ``cu_seqlens[s + 1]`` (int32 on the device; None: one sequence). Returns the outputs in ``q``'s
-    shape and dtype; rows outside every sequence are not written. ``status``: an int64 tensor that
-    collects error bits."""
+    shape and dtype; rows outside every sequence are not written, nor those from the first sequence
+    on whose bounds are inconsistent. ``status``: an int64 tensor that collects error bits."""
     shape = _rank(q, "q", 3)
     rows, nq, hd = shape
     nkv = _rank(k, "k", 3)[1]

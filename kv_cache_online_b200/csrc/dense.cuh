@@ -40,7 +40,7 @@ struct Unit {
   int open;       // first key (prompt: token; tree: cached row) that some row must not see
 };
 
-// Rows [lo, hi) of sequence s; an inconsistent entry counts as empty and is reported.
+// Rows of sequence s from lo on; -1 (reported) if its bounds contradict each other or the rows.
 ISKV_DEV int seq_len(const DenseArgs &a, int s, int64_t &lo) {
   if (!a.cu) {  // one sequence of all rows
     lo = 0;
@@ -50,39 +50,47 @@ ISKV_DEV int seq_len(const DenseArgs &a, int s, int64_t &lo) {
   lo = b;
   if (b < 0 || e < b || e > a.rows) {
     report(a.status, ISKV_ERR_SHAPE);
-    return 0;
+    return -1;
   }
   return (int)(e - b);
 }
 
 // Whole warp: the rank-th unit (without its head) of a prompt call. F(m) = sum over sequences of
 // max(blocks - m, 0) counts the blocks with index >= m; the unit has the largest m with
-// F(m) > rank.
+// F(m) > rank. Sequences count up to the first whose bounds are inconsistent: those before it are
+// disjoint, so that no row belongs to two units and the grid, made for n_rows rows, has a CTA for
+// each.
 template <int ROWS>
 ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   const int lane = threadIdx.x & 31;
   if (a.batch == 1) {
     u.len = seq_len(a, 0, u.base);
     const int n = (int)(((int64_t)u.len * a.group + ROWS - 1) / ROWS);
-    if (rank >= n) return false;
+    if (rank >= n) return false;  // (n <= 0 for -1 rows)
     u.b = 0;
     u.row0 = (n - 1 - rank) * ROWS;
     u.n_rows = min(ROWS, u.len * a.group - u.row0);
     return true;
   }
+  int seqs = a.batch;  // consistent ones, once every lane has looked at its own
   auto blocks = [&](int s) {
+    if (s >= seqs) return 0;
     int64_t lo;
-    return s < a.batch ? (int)(((int64_t)seq_len(a, s, lo) * a.group + ROWS - 1) / ROWS) : 0;
+    const int n = seq_len(a, s, lo);
+    if (n < 0) seqs = s;
+    return (int)(((int64_t)max(n, 0) * a.group + ROWS - 1) / ROWS);
   };
-  const int mine = blocks(lane);  // the first 32 sequences stay in registers
+  int mine = blocks(lane);  // the first 32 sequences stay in registers
   int top = mine;
 #pragma unroll 1
   for (int s = 32 + lane; s < a.batch; s += 32) top = max(top, blocks(s));
-  top = __reduce_max_sync(0xffffffffu, top);
+  top = __reduce_max_sync(0xffffffffu, top);  // (of a sequence that does not count at worst)
+  seqs = __reduce_min_sync(0xffffffffu, seqs);
+  if (lane >= seqs) mine = 0;
   auto F = [&](int m) {
     int n = max(mine - m, 0);
 #pragma unroll 1
-    for (int s = 32 + lane; s < a.batch; s += 32) n += max(blocks(s) - m, 0);
+    for (int s = 32 + lane; s < seqs; s += 32) n += max(blocks(s) - m, 0);
     return __reduce_add_sync(0xffffffffu, n);
   };
   if (top == 0) return false;
@@ -100,7 +108,7 @@ ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   if (lo < 0) return false;
   int skip = rank - above;  // among the sequences with more than lo blocks
 #pragma unroll 1
-  for (int s0 = 0; s0 < a.batch; s0 += 32) {
+  for (int s0 = 0; s0 < seqs; s0 += 32) {
     const unsigned has = __ballot_sync(0xffffffffu, (s0 == 0 ? mine : blocks(s0 + lane)) > lo);
     const int n = __popc(has);
     if (skip >= n) {

@@ -7,8 +7,8 @@ References and element-wise bounds as in ``test_gpu_dense``.
 import pytest
 import torch
 
-from gpu_util import kv, np64
-from test_gpu_dense import (check, i32, tree_inputs, tree_reference)
+from gpu_util import bit, kv, np64
+from test_gpu_dense import SHAPE, check, gen, i32, randn, tree_inputs, tree_reference
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +48,31 @@ def test_work_behind_a_tree_call_without_cut_units(dtype, b, t, cap, n_cached, n
             snap.zero_()
             step()
             assert torch.equal(snap, want)
+
+
+@pytest.mark.parametrize("dtype,hd", [(torch.bfloat16, 128), (torch.float16, 64),
+                                      (torch.float32, 64)])
+@pytest.mark.parametrize("cu,good", [
+    ([0, 1000, 0, 1000], 1),             # the same rows twice
+    ([0, 1000] * 8, 1),
+    ([0, 10, 5, 15, 900], 1),            # overlapping by five rows
+    ([40, 300, 1001, 700, 900], 1),      # beyond the rows, then inside again
+    ([-1, 200, 400, 1000], 0),
+    ([500, 400, 600, 1000], 0),
+    ([300, -1], 0),
+    (list(range(0, 80, 2)) + [0, 500, 1000], 39),  # past the first 32 sequences
+])
+def test_prompt_sequences_count_up_to_the_first_inconsistent_one(dtype, hd, cu, good):
+    """Sequences ahead of the first broken pair are whole, all rows behind stay as they were."""
+    K = kv()
+    rows = 1000
+    q, k, v = (randn(gen(70), rows, h, hd, dtype=dtype) for h in (4, 2, 2))
+    out, status = torch.full_like(q, 7.0), torch.zeros(1, dtype=torch.int64, device="cuda")
+    K.prompt_attention(q, k, v, i32(cu), out=out, status=status)
+    assert status.item() == bit(SHAPE)
+    want = torch.full_like(q, 7.0)
+    if good:
+        status.zero_()
+        K.prompt_attention(q, k, v, i32(cu[:good + 1]), out=want, status=status)
+        assert status.item() == 0
+    assert torch.equal(out, want)
