@@ -15,7 +15,9 @@
  *    (ISKV_ERR_CUDA); nothing is launched when an error is returned.
  *  - Conditions found on the device (capacity, non-finite values, an unconverged Jacobi sweep, a
  *    bounded wait that ran out) are OR-ed into the history's device status word
- *    (meta[ISKV_META_STATUS], bit (1 << code)) and read back with iskv_get_status(), which syncs.
+ *    (meta[ISKV_META_STATUS], bit (1 << code)) and read back with iskv_get_status(), which syncs;
+ *    those of dense attention into the call's status word, or without one into the device's
+ *    (iskv_dense_status()).
  *  - Matrices are row-major. Element types are given by iskv_dtype values.
  */
 #ifndef ISKV_H
@@ -337,8 +339,8 @@ iskv_status iskv_rope(const iskv_heads *x, const int32_t *pos, int64_t n, int32_
  *              on whose two entries break that, all count as empty (nothing of theirs is written),
  *              and ISKV_ERR_SHAPE is recorded in *status. NULL with n_seqs == 1: one sequence of
  *              all rows.
- * status       device int64, or NULL: bits (1 << code) are OR-ed in (ISKV_ERR_SHAPE,
- *              ISKV_ERR_TIMEOUT).
+ * status       device int64: bits (1 << code) are OR-ed in (ISKV_ERR_SHAPE, ISKV_ERR_TIMEOUT: the
+ *              rows of out are undefined). NULL: into the device's own word, iskv_dense_status().
  * out must not overlap the inputs. 0 <= n_rows <= 2^24, 0 <= n_seqs <= 4096, n_q_heads a multiple
  * of n_kv_heads, at most 64 query heads per key/value head (group = n_q_heads / n_kv_heads),
  * n_kv_heads <= 1024, (n_rows * group / 64 + n_seqs) * n_kv_heads < 2^31, head_dim 1..256, scale
@@ -385,6 +387,13 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
                                 int32_t head_dim, float scale, int32_t dtype,
                                 const iskv_heads *out, int64_t *status, void *ws, size_t ws_bytes,
                                 void *stream);
+
+/*
+ * What dense attention recorded on the current device in calls without a status word, since the
+ * last reset: bits (1 << code) into *bits (host). Waits for the device. reset != 0 clears the bits
+ * that were read.
+ */
+iskv_status iskv_dense_status(int64_t *bits, int32_t reset);
 
 /*
  * Cache policy: the exact rows of one side (K or V) of one (sequence, layer), and when its pending

@@ -413,7 +413,8 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
     ``k`` and ``v`` (rows, n_kv, head_dim), rotated; sequence ``s`` is rows ``cu_seqlens[s]`` to
     ``cu_seqlens[s + 1]`` (int32 on the device; None: one sequence). Returns the outputs in ``q``'s
     shape and dtype; rows outside every sequence are not written, nor those from the first sequence
-    on whose bounds are inconsistent. ``status``: an int64 tensor that collects error bits."""
+    on whose bounds are inconsistent. ``status``: an int64 tensor that collects error bits (None:
+    the device's word, :func:`dense_status`)."""
     shape = _rank(q, "q", 3)
     rows, nq, hd = shape
     nkv = _rank(k, "k", 3)[1]
@@ -450,8 +451,8 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     n_kv, head_dim) with ``n_cached`` (batch,) int32 rows in use (None: all). Queries and keys are
     rotated. Node ``i`` sees the cached rows, itself and its ancestors; padding gives zeros. One node
     with parent -1 is plain decoding. Returns the outputs in ``q``'s shape and dtype. ``status``: an
-    int64 tensor that collects error bits; ``ws``: a workspace to use instead of a buffer of the
-    call's own (calls that may overlap need one each)."""
+    int64 tensor that collects error bits (None: the device's word, :func:`dense_status`); ``ws``: a
+    workspace to use instead of a buffer of the call's own (calls that may overlap need one each)."""
     shape = _rank(q, "q", 4)
     b, t, nq, hd = shape
     _, cap, nkv, _ = _rank(k_cache, "k_cache", 4)
@@ -477,6 +478,15 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
             1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, ws.data_ptr(),
             ws.numel() * ws.element_size(), s), "tree_attention")
     return out
+
+
+def dense_status(device=None, reset: bool = True) -> int:
+    """Error bits (``1 << code``) that :func:`prompt_attention` and :func:`tree_attention` recorded
+    on the device in calls without ``status``, since the last reset; waits for the device."""
+    bits = ctypes.c_int64()
+    with torch.cuda.device(device):
+        _lib.check(_lib.load().iskv_dense_status(ctypes.byref(bits), reset), "dense_status")
+    return bits.value
 
 
 def select_workspace_size(L, n_heads, block=8) -> int:

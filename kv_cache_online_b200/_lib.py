@@ -95,6 +95,7 @@ SIGNATURES = {
     "iskv_tree_attention": (c_i32, [c_hp, c_hp, c_hp, c_vp, c_hp, c_hp, c_vp, c_i32, c_i32, c_i64,
                                     c_i32, c_i32, c_i32, c_f32, c_i32, c_hp, c_vp, c_vp, c_sz,
                                     c_vp]),
+    "iskv_dense_status": (c_i32, [ctypes.POINTER(c_i64), c_i32]),
     "iskv_cache_prefill_workspace_size": (c_sz, [c_i32]),
     "iskv_cache_prefill": (c_i32, [ctypes.POINTER(IskvExactTable), c_vp, c_i32, c_i64, c_vp, c_i64,
                                    c_i32, c_vp, c_vp, ctypes.POINTER(c_i64), c_vp, c_sz, c_vp]),

@@ -20,10 +20,10 @@
 namespace iskv {
 namespace dense {
 
-// status: one int64 word (or NULL), bit (1 << code).
+// status: one int64 word, bit (1 << code).
 // (Out of line: the callers run once per unit, and their instructions come from L2 each time.)
 static __device__ __noinline__ void report(int64_t *status, int code) {
-  if (status) atomicOr(reinterpret_cast<unsigned long long *>(status), 1ull << code);
+  atomicOr(reinterpret_cast<unsigned long long *>(status), 1ull << code);
 }
 
 // One unit's place: tiles [t0, t1) of its n_tiles.

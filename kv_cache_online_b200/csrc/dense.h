@@ -28,7 +28,7 @@ struct DenseArgs {
   int32_t n_q, n_kv, group, head_dim;
   float scale;
   int32_t dtype;
-  int64_t *status;          // may be NULL
+  int64_t *status;
   void *ws;                 // tree: partial results
 };
 

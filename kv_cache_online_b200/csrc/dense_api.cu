@@ -1,5 +1,6 @@
 // C ABI of the rotary embedding and the dense attention (see include/iskv.h): argument checks, the
 // choice between the tensor-core and the CUDA-core kernel, launches.
+#include <atomic>
 #include <cmath>
 
 #include "api_error.h"
@@ -9,6 +10,29 @@
 using namespace iskv;
 
 namespace {
+
+// What calls without a status word of their own record, one word per device.
+__device__ unsigned long long g_status;
+
+__global__ void k_clear_status(unsigned long long bits) { atomicAnd(&g_status, ~bits); }
+
+// `status`, or the current device's own word (looked up once per device, the first 64).
+cudaError_t status_word(int64_t *status, int64_t **word) {
+  static std::atomic<int64_t *> known[64];
+  *word = status;
+  if (status) return cudaSuccess;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64) *word = known[dev].load(std::memory_order_relaxed);
+  if (*word) return cudaSuccess;
+  void *p = nullptr;
+  e = cudaGetSymbolAddress(&p, g_status);
+  if (e != cudaSuccess) return e;
+  *word = static_cast<int64_t *>(p);
+  if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
+  return cudaSuccess;
+}
 
 size_t elem_bytes(int32_t t) { return t == ISKV_F32 ? 4 : 2; }
 
@@ -58,8 +82,9 @@ iskv_status check_status_word(const int64_t *status, const char *who) {
   return ISKV_OK;
 }
 
-cudaError_t launch_dense(const DenseArgs &a, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
+cudaError_t launch_dense(DenseArgs &a, cudaStream_t s) {
+  cudaError_t e = status_word(a.status, &a.status);
+  if (e != cudaSuccess) return e;
   if (dense_tc_takes(a) && launch_dense_tc(a, s, e)) return e;
   return launch_dense_cc(a, s);
 }
@@ -252,6 +277,25 @@ iskv_status iskv_tree_attention(const iskv_heads *q, const iskv_heads *k_draft,
   cudaError_t e = launch_dense(a, s);
   if (e != cudaSuccess) return cuda_fail(e, who);
   stage_mark(s, ST_TREE_ATTN);
+  return ISKV_OK;
+}
+
+iskv_status iskv_dense_status(int64_t *bits, int32_t reset) {
+  const char *who = "iskv_dense_status";
+  clear_last_error();
+  if (!bits) return fail(ISKV_ERR_ARG, "%s: null output", who);
+  // (The word's kernels may run on streams that the legacy default stream does not wait for.)
+  cudaError_t e = cudaDeviceSynchronize();
+  unsigned long long word = 0;
+  if (e == cudaSuccess) e = cudaMemcpyFromSymbol(&word, g_status, sizeof word);
+  if (e == cudaSuccess && reset && word) {
+    k_clear_status<<<1, 1>>>(word);
+    count_launches(1);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = cudaDeviceSynchronize();
+  }
+  if (e != cudaSuccess) return cuda_fail(e, who);
+  *bits = (int64_t)word;
   return ISKV_OK;
 }
 

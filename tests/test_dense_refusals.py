@@ -124,3 +124,9 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     with pytest.raises(ValueError):
         kv.tree_attention(x[None], x[None], x[None], pos[None], x[None], x[None])
     assert ctypes.sizeof(kv.IskvHeads) == 32
+
+
+def test_the_device_s_error_word_needs_a_place():
+    _, lib = _lib()
+    assert lib.iskv_dense_status(None, 1) == ARG
+    assert lib.iskv_last_error().startswith(b"iskv_dense_status")

@@ -4,9 +4,14 @@ contradict each other, extreme scales, errors without a status word, and the acc
 References and element-wise bounds as in ``test_gpu_dense``.
 """
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
+from conftest import ROOT
 from gpu_util import bit, kv, np64
 from test_gpu_dense import SHAPE, check, gen, i32, randn, tree_inputs, tree_reference
 
@@ -76,3 +81,44 @@ def test_prompt_sequences_count_up_to_the_first_inconsistent_one(dtype, hd, cu, 
         K.prompt_attention(q, k, v, i32(cu[:good + 1]), out=want, status=status)
         assert status.item() == 0
     assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_errors_without_a_status_word_are_kept_by_the_device(dtype):
+    K = kv()
+    K.dense_status()
+    q = randn(gen(71), 64, 2, 64, dtype=dtype)
+    K.prompt_attention(q, q, q)
+    K.tree_attention(q[None], q[None], q[None], i32([list(range(-1, 63))]), q[None], q[None])
+    assert K.dense_status() == 0
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    K.prompt_attention(q, q, q, i32([0, 10, 5]), stream=s)
+    assert K.dense_status(reset=False) == K.dense_status("cuda:0") == bit(SHAPE)
+    assert K.dense_status() == 0
+    for parents, n in ([list(range(64)), 64], [list(range(-1, 63)), 65]):
+        K.tree_attention(q[None], q[None], q[None], i32([parents]), q[None], q[None], i32([n]))
+        assert K.dense_status() == bit(SHAPE)
+    status = torch.zeros(1, dtype=torch.int64, device="cuda")
+    K.prompt_attention(q, q, q, i32([0, 10, 5]), status=status)
+    assert K.dense_status() == 0 and status.item() == bit(SHAPE)
+
+
+def test_the_first_call_of_a_process_may_be_captured():
+    """Kernels and the device's error word are found while a stream is captured."""
+    kv()
+    code = """
+import torch, kv_cache_online_b200 as K
+for dtype in (torch.bfloat16, torch.float32):
+    q = torch.randn(64, 2, 64, device="cuda").to(dtype)
+    cu = torch.tensor([0, 10, 5], dtype=torch.int32, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = K.prompt_attention(q, q, q, cu)
+    g.replay()
+    assert K.dense_status() == 4, K.dense_status()
+    assert torch.equal(out[:10], K.prompt_attention(q[:10], q[:10], q[:10]))
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=os.environ, capture_output=True,
+                       text=True, timeout=300)
+    assert r.returncode == 0, r.stderr
