@@ -466,6 +466,8 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     pp = _ints(parents, "parents", (b, t), dev)
     npp = None if n_cached is None else _ints(n_cached, "n_cached", (b,), dev)
     sw = _status_word(status, dev)
+    if ws is not None and (ws.get_device() != dev.index or not ws.is_contiguous()):
+        raise ValueError(f"ws must be a contiguous tensor on {dev}")
     lib = _lib.load()
     with _On(dev, stream) as s:
         out, ho = _written(out, q, "out", shape, dtype, dev)

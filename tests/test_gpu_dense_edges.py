@@ -122,3 +122,24 @@ for dtype in (torch.bfloat16, torch.float32):
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, env=os.environ, capture_output=True,
                        text=True, timeout=300)
     assert r.returncode == 0, r.stderr
+
+
+def test_a_workspace_of_the_caller_s():
+    K = kv()
+    q, kd, vd, kc, vc = tree_inputs(72, torch.bfloat16, 2, 5, 1000, 4, 2, 64)
+    par = i32([[-1, 0, 1, 1, 0]] * 2)
+    n = K.tree_attention_workspace_size(5, 4, 2, 64)
+    for ws in (torch.empty(n, dtype=torch.uint8), torch.empty(n, dtype=torch.uint8).pin_memory(),
+               torch.empty(2 * n, dtype=torch.uint8, device="cuda")[::2],
+               torch.empty(1, dtype=torch.uint8, device="cuda").expand(n)):
+        with pytest.raises(ValueError):
+            K.tree_attention(q, kd, vd, par, kc, vc, ws=ws)
+    for ws in (torch.empty(0, dtype=torch.uint8, device="cuda"),
+               torch.empty(n - 1, dtype=torch.uint8, device="cuda"),
+               torch.empty(n + 16, dtype=torch.uint8, device="cuda")[16:]):
+        with pytest.raises(K.IskvError):
+            K.tree_attention(q, kd, vd, par, kc, vc, ws=ws)
+    # a tensor of any type and shape with enough bytes behind it
+    ws = torch.empty(-(-n // 80), 10, dtype=torch.float64, device="cuda")
+    want = K.tree_attention(q, kd, vd, par, kc, vc)
+    assert torch.equal(K.tree_attention(q, kd, vd, par, kc, vc, ws=ws), want)
