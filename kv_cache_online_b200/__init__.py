@@ -321,10 +321,6 @@ def decode_attention(k_hist, v_hist, k_exact, k_exact_pos, v_exact, v_exact_pos,
 # Dense attention around the compressed cache: the rotary embedding, the prompt's exact attention
 # (where Algorithm 1 starts) and drafted tokens over a reconstructed cache (Algorithm 3 step 9).
 
-# (torch.cuda.current_stream() builds a stream object, 3 us of a short call's time.)
-_raw_stream = torch._C._cuda_getCurrentRawStream
-
-
 class _On:
     """The device and stream of a call: ``with _On(device, stream) as s`` makes the device current
     and allocates on the stream; ``s`` is its raw handle."""
@@ -341,7 +337,8 @@ class _On:
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        return _raw_stream(self.device.index)
+        # (torch.cuda.current_stream() builds a stream object, 3 us of a short call's time.)
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:

@@ -1,9 +1,13 @@
 """What the rotary embedding and the dense attention refuse, on the host before any CUDA call."""
 
 import ctypes
+import subprocess
+import sys
 
 import pytest
 import torch
+
+from conftest import ROOT
 
 
 def _lib():
@@ -130,3 +134,15 @@ def test_the_device_s_error_word_needs_a_place():
     _, lib = _lib()
     assert lib.iskv_dense_status(None, 1) == ARG
     assert lib.iskv_last_error().startswith(b"iskv_dense_status")
+
+
+def test_the_package_loads_without_cuda_in_torch():
+    """The entry points of the host (workspace queries, plans) need no CUDA build of torch."""
+    _lib()
+    code = ("import torch\n"
+            "for name in dir(torch._C):\n"
+            "    if name.startswith('_cuda_getCurrent'): delattr(torch._C, name)\n"
+            "import kv_cache_online_b200 as kv\n"
+            "assert kv.tree_attention_workspace_size(16, 32, 8, 128) > 0\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
