@@ -343,8 +343,9 @@ iskv_status iskv_rope(const iskv_heads *x, const int32_t *pos, int64_t n, int32_
  *              rows of out are undefined). NULL: into the device's own word, iskv_dense_status().
  * out must not overlap the inputs. 0 <= n_rows <= 2^24, 0 <= n_seqs <= 4096, n_q_heads a multiple
  * of n_kv_heads, at most 64 query heads per key/value head (group = n_q_heads / n_kv_heads),
- * n_kv_heads <= 1024, (n_rows * group / 64 + n_seqs) * n_kv_heads < 2^31, head_dim 1..256, scale
- * finite. Softmax and sums are float32; on the tensor cores the probabilities enter the
+ * n_kv_heads <= 1024, (n_rows * group / 64 + n_seqs) * n_kv_heads < 2^31, head_dim 1..256, |scale|
+ * at most 2^127. q . k and scale log2(e) q . k are float32 and have to stay within its range.
+ * Softmax and sums are float32; on the tensor cores the probabilities enter the
  * second product in the element type.
  */
 iskv_status iskv_prompt_attention(const iskv_heads *q, const iskv_heads *k, const iskv_heads *v,

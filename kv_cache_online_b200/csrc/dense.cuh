@@ -126,6 +126,13 @@ ISKV_DEV bool find_prompt_unit(const DenseArgs &a, int rank, Unit &u) {
   return true;
 }
 
+// |scale| log2(e), the factor on the scores (its sign goes into the queries). Never 0, because
+// masked scores are -inf: with scale 0 it is the smallest float, 2^-149, which takes any finite
+// score to 2^-21 or less.
+ISKV_DEV float score_factor(const DenseArgs &a) {
+  return fmaxf(fabsf(a.scale) * 1.4426950408889634f, __int_as_float(1));
+}
+
 // Tokens of the first and last row of a block.
 ISKV_DEV int first_token(const DenseArgs &a, const Unit &u) { return u.row0 / a.group; }
 ISKV_DEV int last_token(const DenseArgs &a, const Unit &u) {

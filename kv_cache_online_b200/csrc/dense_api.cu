@@ -72,7 +72,9 @@ iskv_status check_shape(int32_t n_q, int32_t n_kv, int32_t head_dim, float scale
                 "per key/value head (got %d, %d)", who, n_q, n_kv);
   if (head_dim < 1 || head_dim > 256)
     return fail(ISKV_ERR_SHAPE, "%s: need 1 <= head_dim <= 256 (got %d)", who, head_dim);
-  if (!std::isfinite(scale)) return fail(ISKV_ERR_ARG, "%s: scale must be finite", who);
+  // (scale log2(e) has to be finite too)
+  if (!(std::fabs(scale) <= 0x1p127f))
+    return fail(ISKV_ERR_ARG, "%s: scale must be finite, 2^127 at most in magnitude", who);
   return ISKV_OK;
 }
 

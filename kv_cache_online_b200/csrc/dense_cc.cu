@@ -21,7 +21,6 @@ namespace {
 using namespace dense;
 
 constexpr int ROWS = DENSE_CC_ROWS, KT = 64, NT = 256;
-constexpr float LOG2E = 1.4426950408889634f;
 
 template <int HD, int BUF>
 struct Smem {
@@ -95,7 +94,7 @@ ISKV_DEV void run_unit(const DenseArgs &a, Smem<HD, BUFFERS<T, HD, VEC>> &sm, co
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
   const int hd = a.head_dim;
   // Non-negative factor on the scores; the scale's sign goes into the queries.
-  const float c = fmaxf(fabsf(a.scale) * LOG2E, 1e-30f);  // (not 0: masked scores are -inf)
+  const float c = score_factor(a);
   const int64_t row_base = TREE ? 0 : u.base;
 
   for (int i = threadIdx.x; i < ROWS * HD; i += NT) {

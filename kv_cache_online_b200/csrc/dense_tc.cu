@@ -50,7 +50,6 @@ using namespace dense;
 using namespace tc;
 
 constexpr int KT = 128;
-constexpr float LOG2E = 1.4426950408889634f;
 constexpr uint64_t WAIT_NS = 2000000000ull;
 constexpr float LAZY = 8.f;  // log2 of the growth of a row's maximum that is left in P
 enum { MODE_PROMPT = 0, MODE_ROWS = 1, MODE_KEYS = 2 };
@@ -347,7 +346,7 @@ __global__ void __launch_bounds__(384, 1)
     const int row = quad * 32 + lane;             // row of the stream's tile
     const uint32_t lanes = (uint32_t)quad << 21;  // TMEM lane base of the warp
     const uint32_t o_tm = tmem + lanes + O_COL + HD * st;
-    const float c = fmaxf(fabsf(a.scale) * LOG2E, 1e-30f);
+    const float c = score_factor(a);
     constexpr float BIAS = std::is_same<T, __half>::value ? 6.f : 0.f;
     char *q_tile = base + (MODE == MODE_KEYS ? 0 : st) * C::TILE;
     const int row_off = MODE == MODE_KEYS ? 0 : 128 * st;  // first unit row of the tile
@@ -459,7 +458,7 @@ __global__ void __launch_bounds__(384, 1)
             l *= f;
             m = to;
             off = BIAS - (m == -INFINITY ? 0.f : m * c);
-            top_lim = m + LAZY / c;
+            top_lim = m + fminf(LAZY / c, 3e38f);  // (-inf while m is, whatever c)
             if (i > 0) {
               // The stream's previous product must have left O. (The one before it has: S(i) was
               // issued behind it. The next one waits for this warp.)

@@ -146,3 +146,9 @@ def test_the_package_loads_without_cuda_in_torch():
             "assert kv.tree_attention_workspace_size(16, 32, 8, 128) > 0\n")
     r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+def test_scales_beyond_2_to_127_are_refused():
+    L, lib = _lib()
+    for scale in (3e38, -3e38, 2.0 ** 127 * (1 + 2.0 ** -23)):
+        assert _prompt(L, lib, scale=scale) == ARG and _tree(L, lib, scale=scale) == ARG

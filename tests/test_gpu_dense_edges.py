@@ -13,7 +13,8 @@ import torch
 
 from conftest import ROOT
 from gpu_util import bit, kv, np64
-from test_gpu_dense import SHAPE, check, gen, i32, randn, tree_inputs, tree_reference
+from test_gpu_dense import (SHAPE, check, gen, i32, prompt_reference, randn, tree_inputs,
+                            tree_reference)
 
 pytestmark = pytest.mark.gpu
 
@@ -143,3 +144,26 @@ def test_a_workspace_of_the_caller_s():
     ws = torch.empty(-(-n // 80), 10, dtype=torch.float64, device="cuda")
     want = K.tree_attention(q, kd, vd, par, kc, vc)
     assert torch.equal(K.tree_attention(q, kd, vd, par, kc, vc, ws=ws), want)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("scale,gain", [(1e-33, 1e33), (-2.0 ** -115, 2.0 ** 115), (0.0, 1e35),
+                                        (1e-40, 1e35), (1e30, 1e-30), (2.0 ** 127, 2.0 ** -125)])
+def test_scales_far_from_one(dtype, scale, gain):
+    """Tiny scales of huge scores, the largest scale, and 0 whatever the scores: weights still follow
+    the product of the two. Rows of the first sequence see only keys ahead of the second's."""
+    K = kv()
+    nq, nkv, hd, lens = 4, 2, 64, [70, 300]
+    g, n = gen(73), 370
+    q, k, v = (randn(g, n, h, hd, dtype=dtype) for h in (nq, nkv, nkv))
+    q *= gain
+    got = K.prompt_attention(q, k, v, i32([0, 70, 370]), scale)
+    ref, mag, smax = prompt_reference(np64(q), np64(k), np64(v), [0, 70, 370], scale)
+    check(np64(got), ref, mag, smax, max(lens), hd, dtype)
+    for t in (5, 100):  # both splits of a tree's rows
+        par = [list(range(-1, t - 1))]
+        args = [x[:t][None] for x in (q, k, v)]
+        got = K.tree_attention(*args, i32(par), k[None], v[None], i32([300]), scale)
+        ref, mag, smax = tree_reference(*map(np64, args), par, np64(k[None]), np64(v[None]), [300],
+                                        scale)
+        check(np64(got), ref, mag, smax, 300 + t, hd, dtype)
