@@ -383,6 +383,10 @@ def _written(out, t: torch.Tensor, name: str, shape, dtype, device):
     return out, IskvHeads(out.data_ptr(), shape[-3] * row, row, shape[-1])
 
 
+def _scale(scale, head_dim: int) -> float:
+    return 1.0 / math.sqrt(max(head_dim, 1)) if scale is None else scale
+
+
 def _rank(t: torch.Tensor, name: str, n: int):
     if t.dim() != n:
         raise ValueError(f"{name}: {t.dim()} axes, expected {n}")
@@ -429,7 +433,7 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
         out, ho = _written(out, q, "out", shape, dtype, dev)
         _lib.check(_lib.load().iskv_prompt_attention(
             hq, hk, hv, cp, seqs, rows, nq, nkv, hd,
-            1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, s), "prompt_attention")
+            _scale(scale, hd), dt, ho, sw, s), "prompt_attention")
     return out
 
 
@@ -474,7 +478,7 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
             ws = q.new_empty(tree_attention_workspace_size(t, nq, nkv, hd) // q.element_size())
         _lib.check(lib.iskv_tree_attention(
             hq, hkd, hvd, pp, hkc, hvc, npp, b, t, cap, nq, nkv, hd,
-            1.0 / math.sqrt(hd) if scale is None else scale, dt, ho, sw, ws.data_ptr(),
+            _scale(scale, hd), dt, ho, sw, ws.data_ptr(),
             ws.numel() * ws.element_size(), s), "tree_attention")
     return out
 

@@ -167,3 +167,13 @@ def test_scales_far_from_one(dtype, scale, gain):
         ref, mag, smax = tree_reference(*map(np64, args), par, np64(k[None]), np64(v[None]), [300],
                                         scale)
         check(np64(got), ref, mag, smax, 300 + t, hd, dtype)
+
+
+def test_heads_without_elements_are_refused_by_the_library():
+    K = kv()
+    x = torch.empty(4, 2, 0, device="cuda")
+    for call in (lambda: K.prompt_attention(x, x, x),
+                 lambda: K.tree_attention(x[None], x[None], x[None], i32([[-1, 0, 1, 2]]), x[None],
+                                          x[None])):
+        with pytest.raises(K.IskvError):
+            call()
