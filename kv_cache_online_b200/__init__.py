@@ -322,14 +322,18 @@ def decode_attention(k_hist, v_hist, k_exact, k_exact_pos, v_exact, v_exact_pos,
 # (where Algorithm 1 starts) and drafted tokens over a reconstructed cache (Algorithm 3 step 9).
 
 class _On:
-    """The device and stream of a call: ``with _On(device, stream) as s`` makes the device current
-    and allocates on the stream; ``s`` is its raw handle."""
+    """The device and stream of a call: ``with _On(device, stream, *tensors) as s`` makes the device
+    current and allocates on the stream; ``s`` is its raw handle. Memory of tensors used on a given
+    stream is not handed out again before the stream is done with it, whoever drops them."""
 
-    def __init__(self, device, stream):
+    def __init__(self, device, stream, *tensors):
         self.device, self.ctx = device, None
         if stream is not None:
             if stream.device != device:
                 raise ValueError("the stream belongs to another device than the tensors")
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
             self.ctx = torch.cuda.stream(stream)  # also makes its device current
         elif device.index != torch.cuda.current_device():
             self.ctx = torch.cuda.device(device)
@@ -403,7 +407,7 @@ def apply_rope(x, pos, theta: float = 500000.0, inverse: bool = False, out=None,
     hx = _heads(x, "x", shape, x.dtype, dev)
     dt = _dt(x)
     pp = _ints(pos, "pos", (n,), dev)
-    with _On(dev, stream) as s:
+    with _On(dev, stream, x, pos, out) as s:
         out, ho = _written(out, x, "out", shape, x.dtype, dev)
         _lib.check(_lib.load().iskv_rope(hx, pp, n, heads, hd, theta, inverse, dt, ho, s), "rope")
     return out
@@ -425,11 +429,11 @@ def prompt_attention(q, k, v, cu_seqlens=None, scale=None, out=None, status=None
     hk = _heads(k, "k", (rows, nkv, hd), dtype, dev)
     hv = _heads(v, "v", (rows, nkv, hd), dtype, dev)
     sw = _status_word(status, dev)
-    with _On(dev, stream) as s:
-        seqs, cp = 1, None
-        if cu_seqlens is not None:
-            seqs = max(cu_seqlens.numel() - 1, 0)
-            cp = _ints(cu_seqlens, "cu_seqlens", (seqs + 1,), dev)
+    seqs, cp = 1, None
+    if cu_seqlens is not None:
+        seqs = max(cu_seqlens.numel() - 1, 0)
+        cp = _ints(cu_seqlens, "cu_seqlens", (seqs + 1,), dev)
+    with _On(dev, stream, q, k, v, cu_seqlens, out, status) as s:
         out, ho = _written(out, q, "out", shape, dtype, dev)
         _lib.check(_lib.load().iskv_prompt_attention(
             hq, hk, hv, cp, seqs, rows, nq, nkv, hd,
@@ -470,7 +474,8 @@ def tree_attention(q, k_draft, v_draft, parents, k_cache, v_cache, n_cached=None
     if ws is not None and (ws.get_device() != dev.index or not ws.is_contiguous()):
         raise ValueError(f"ws must be a contiguous tensor on {dev}")
     lib = _lib.load()
-    with _On(dev, stream) as s:
+    with _On(dev, stream, q, k_draft, v_draft, parents, k_cache, v_cache, n_cached, out, status,
+             ws) as s:
         out, ho = _written(out, q, "out", shape, dtype, dev)
         if ws is None:
             # A buffer of this call's own, from the stream's pool: calls on several streams and

@@ -177,3 +177,32 @@ def test_heads_without_elements_are_refused_by_the_library():
                                           x[None])):
         with pytest.raises(K.IskvError):
             call()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_tensors_dropped_while_another_stream_still_reads_them(dtype):
+    """Temporaries of the current stream in a call on another one that is busy: dropped right after
+    the call, their memory asked for and overwritten at once."""
+    K = kv()
+    q, kd, vd, kc, vc = tree_inputs(74, dtype, 2, 9, 1500, 4, 2, 64)
+    par, nc = i32([[-1, 0, 1, 0, 3, 3, 2, 7, 7]] * 2), i32([1500, 321])
+    pos = torch.arange(9, dtype=torch.int32, device="cuda")
+    calls = [
+        (lambda a, s: K.tree_attention(*a, stream=s), (q, kd, vd, par, kc, vc, nc)),
+        (lambda a, s: K.prompt_attention(*a, stream=s), (kc[0], kc[1], vc[0], i32([0, 700, 1500]))),
+        (lambda a, s: K.apply_rope(*a, stream=s), (q[0], pos)),
+    ]
+    s = torch.cuda.Stream()
+    for call, args in calls:
+        want = call(args, None)
+        temps = [x.clone() for x in args]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(50_000_000)
+        got = call(temps, s)
+        sizes = [x.numel() * x.element_size() for x in temps]
+        del temps
+        junk = [torch.full((n,), 0xff, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+        del junk
