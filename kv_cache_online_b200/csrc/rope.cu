@@ -4,7 +4,9 @@
 // x'[j + hd/2] = x[j + hd/2] cos a + x[j] sin a,   a = +-pos * theta^(-2j/hd).
 //
 // Angles: w_j = theta^(-2j/hd) / 2 pi turns per position as a 0.64 fixed-point fraction; pos * w_j
-// modulo 2^64 is the angle modulo one turn, exact but for w_j's own rounding (pos * 2^-65 turns).
+// modulo 2^64 is the angle modulo one turn, exact but for w_j's own error (for theta >= 1 less than
+// pos * 2^-63 turns: the truncation, and half of that again from its 64-bit logarithm and
+// exponential).
 // The two top bits after rounding pick the quadrant, the rest (|r| <= 1/8 turn) goes to the sine
 // and cosine: CUDA's sincospif for float32, the hardware's for two-byte elements, whose own
 // rounding (2^-12 and up) is far above the hardware's 2^-21.

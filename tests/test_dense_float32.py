@@ -8,7 +8,8 @@ Root mean square, relative. Roundings are independent. A score is a chain of hd 
 roundings of partial sums of size up to 1, together at most u sqrt(hd). Its product with log2(e), up
 to 8, rounds by 8 u at most, and the hardware exponential by 4 u. These act on the weights, one by
 one, so on the output in the same proportion. The sums over n keys round n times, by u of partial
-sums that are no larger than the output's own size but for common direction: u sqrt(n). Twice all that:
+sums that are no larger than the output's own size but for common direction: u sqrt(n). Twice all
+that:
     |got - ref| <= 2 u (sqrt(hd) + 12 + sqrt(n)) |ref|   (Frobenius).
 
 Element by element: ``test_gpu_dense``'s bound with S = |scale| max_j sum_d |q_d k_jd| over the keys

@@ -150,8 +150,8 @@ def test_a_workspace_of_the_caller_s():
 @pytest.mark.parametrize("scale,gain", [(1e-33, 1e33), (-2.0 ** -115, 2.0 ** 115), (0.0, 1e35),
                                         (1e-40, 1e35), (1e30, 1e-30), (2.0 ** 127, 2.0 ** -125)])
 def test_scales_far_from_one(dtype, scale, gain):
-    """Tiny scales of huge scores, the largest scale, and 0 whatever the scores: weights still follow
-    the product of the two. Rows of the first sequence see only keys ahead of the second's."""
+    """Tiny scales of huge scores, the largest scale, and 0 whatever the scores: weights still
+    follow the product of the two."""
     K = kv()
     nq, nkv, hd, lens = 4, 2, 64, [70, 300]
     g, n = gen(73), 370
