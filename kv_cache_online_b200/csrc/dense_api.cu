@@ -1,6 +1,5 @@
 // C ABI of the rotary embedding and the dense attention (see include/iskv.h): argument checks, the
 // choice between the tensor-core and the CUDA-core kernel, launches.
-#include <atomic>
 #include <cmath>
 
 #include "api_error.h"
@@ -16,22 +15,12 @@ __device__ unsigned long long g_status;
 
 __global__ void k_clear_status(unsigned long long bits) { atomicAnd(&g_status, ~bits); }
 
-// `status`, or the current device's own word (looked up once per device, the first 64).
+// `status`, or the current device's own word.
 cudaError_t status_word(int64_t *status, int64_t **word) {
-  static std::atomic<int64_t *> known[64];
-  *word = status;
-  if (status) return cudaSuccess;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev < 64) *word = known[dev].load(std::memory_order_relaxed);
-  if (*word) return cudaSuccess;
-  void *p = nullptr;
-  e = cudaGetSymbolAddress(&p, g_status);
-  if (e != cudaSuccess) return e;
+  void *p = status;
+  const cudaError_t e = status ? cudaSuccess : cudaGetSymbolAddress(&p, g_status);
   *word = static_cast<int64_t *>(p);
-  if (dev < 64) known[dev].store(*word, std::memory_order_relaxed);
-  return cudaSuccess;
+  return e;
 }
 
 size_t elem_bytes(int32_t t) { return t == ISKV_F32 ? 4 : 2; }
